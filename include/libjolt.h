@@ -253,6 +253,155 @@ jolt_status jolt_attention_workspace_size(const jolt_attn_group *groups, int32_t
 jolt_status jolt_decode_attention(jolt_handle h, const jolt_attn_group *groups, int32_t n, int32_t q_heads,
                                   float scale, void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---- token cache: the tokens after the compressed prefill ------------------ */
+/* A payload holds a prefill; the tokens decoded after it are kept in a paged,
+ * quantized cache, one per layer, which jolt_cache_append writes,
+ * jolt_cache_attention and jolt_tree_attention attend over and jolt_cache_read
+ * turns back into rows (for attention elsewhere, or for jolt_plan /
+ * jolt_compress once the tail is long).
+ *
+ * Stored form of a K or V row x of d features: y = x or, with `rotate`, the
+ * seeded rotation y = (1/sqrt d) H (s o x) of the residual codec (signs from
+ * seed and k_item_id or v_item_id); each group of 64 is quantized as the codec
+ * does: scale = bf16(amax / qmax), qmax = 2^(bits-1) - 1, q = clamp(rint(y inv))
+ * with inv = fl32(1 / scale), code q + 2^(bits-1); a scale below 2^-126 is
+ * stored as 0 with q = 0.
+ * The rotation is summed in fp64 and rounded to fp32 once, so for bf16 rows the
+ * codes do not depend on an order of summation.  A row with an infinity or a
+ * NaN gets NaN scales and reads back as NaN.
+ *
+ * Pool: `pages` pages; page p, head h at byte (p H + h) * (bytes of a page /
+ * H), there [K codes | V codes | K scales | V scales] with P = page_tokens:
+ *   K codes   P rows of d bits / 8 bytes; unit g (d/32) + k of a row (g < 4,
+ *             k < d/32) holds features 32 k + 8 g + e, e = 0..7
+ *   V codes   P / 8 blocks of 8 tokens; unit f of a block holds feature f of
+ *             tokens 8 blk + e, e = 0..7
+ *   a unit is 8 bytes (8 bits; byte e) or one little-endian 32-bit word
+ *   (4 bits; member e in the nibble at bit 4 (e/2 + 4 (e mod 2)))
+ *   scales    bf16 [d/64][P]
+ * so that a wave's matrix-core fragments of either are whole 16-byte loads.
+ *
+ *   table   device int32 [batch][max_pages]: page numbers of a sequence's
+ *           tokens, in order.  Tokens in entries outside [0, pages), or past
+ *           the row, are not written and not attended, and read as zeros.
+ *   lens    device int32 [batch]: tokens of each sequence, the rows of the
+ *           present call included: row i of n of sequence b is token
+ *           lens[b] - n + i.
+ * A page may serve several sequences (a shared prefix), but only one of them
+ * may write to it in a call.  Table, lens and the other device arrays are read
+ * by the kernels, never on the host, so a captured call follows them. */
+typedef struct {
+    int32_t H, d;
+    int32_t bits;            /* 4 or 8                                          */
+    int32_t page_tokens;     /* 32, 64, 128 or 256                              */
+    int32_t pages;
+    int32_t max_pages;       /* row length of table                             */
+    int32_t rotate;
+    uint32_t k_item_id, v_item_id;
+    uint32_t reserved;
+    uint64_t seed;
+    void *pool;              /* device, 16-byte aligned, jolt_cache_pool_bytes() */
+    uint64_t pool_bytes;
+    const int32_t *table;
+    const int32_t *lens;
+} jolt_cache;
+
+/* Rows of d features, the features contiguous: row of token i and head h at
+ * ptr + i token_stride + h head_stride (in elements; pointer and strides
+ * multiples of 16 bytes).  Token-major [n][H][d], head-major [H][n][d] and
+ * padded forms of both; rows of an output must not overlap. */
+typedef struct {
+    void *ptr;
+    int64_t token_stride, head_stride;
+} jolt_rows;
+
+jolt_status jolt_cache_pool_bytes(const jolt_cache *cache, size_t *bytes);
+
+/* Write `total` K and V rows (dtype JOLT_BF16 or JOLT_F32): rows starts[b] ..
+ * starts[b+1] - 1 (device int32 [batch + 1]) become the last tokens of sequence
+ * b.  max_new: no sequence has more rows than this (the grid; rows beyond it
+ * are not written).  Rows past starts[batch] are not read. */
+jolt_status jolt_cache_append(jolt_handle h, const jolt_cache *cache, int32_t batch, const int32_t *starts,
+                              int32_t total, int32_t max_new, int32_t dtype, const jolt_rows *k, const jolt_rows *v,
+                              void *stream);
+
+/* Read rows back: row starts[b] + i receives token first[b] + i of sequence b
+ * (first: device int32 [batch], NULL = 0), rounded to dtype; zeros for tokens
+ * outside [0, lens[b]).  max_rows as max_new.  Rows past starts[batch] are left
+ * as they are. */
+jolt_status jolt_cache_read(jolt_handle h, const jolt_cache *cache, int32_t batch, const int32_t *first,
+                            const int32_t *starts, int32_t total, int32_t max_rows, int32_t dtype,
+                            const jolt_rows *k, const jolt_rows *v, void *stream);
+
+/* Keep an accepted path of drafted tokens: token base[b] + path[starts[b] + i]
+ * of sequence b becomes its token base[b] + i, for i < starts[b+1] - starts[b]
+ * (device int32 arrays; base [batch], starts [batch + 1], path [total]; at most
+ * 64 entries of a sequence count).  All are read before any is written, so any
+ * order and repeats are fine.  Entries outside 0..63, or that lead outside the
+ * sequence's pages, leave their token as it was.  lens is not read; the caller
+ * sets it to base + kept. */
+jolt_status jolt_cache_keep(jolt_handle h, const jolt_cache *cache, int32_t batch, const int32_t *base,
+                            const int32_t *starts, const int32_t *path, int32_t total, void *stream);
+
+/* Scores of query row i (position pos_i) and token t (position t):
+ *   s = scale q . k_t;  cap > 0: s = cap tanh(s / cap);  s -= slope |pos_i - t|
+ * over the tokens visible to the row:
+ *   t < lens[b], t >= first_i, and (t < prefix_b or (t <= pos_i and
+ *   (window == 0 or pos_i - t < window)))
+ * so `first` masks earlier documents of a packed sequence and `prefix` is seen
+ * by every row (a prompt read both ways, or kept first tokens of a window).
+ * A row that sees nothing gets zeros and lse = -infinity.
+ *   slopes  device fp32 [q_heads] or NULL     prefix  device int32 [batch] or NULL
+ *   first   device int32 [total] or NULL
+ *   merge_out, merge_lse  device fp32 [total][q_heads][d], [total][q_heads], or
+ *           both NULL: another part's attention, e.g. jolt_decode_attention's
+ *           over the payloads of the same sequence, joined into the result by
+ *           the two log-sum-exps */
+typedef struct {
+    float scale;
+    float cap;
+    int32_t window;
+    int32_t reserved;
+    const float *slopes;
+    const int32_t *prefix;
+    const int32_t *first;
+    const float *merge_out;
+    const float *merge_lse;
+} jolt_attn_terms;
+
+/* Attention of `total` query rows (bf16, q_heads heads, a multiple of H: query
+ * head j reads KV head j / (q_heads / H)) over the cache: rows starts[b] ..
+ * starts[b+1] - 1 are the last tokens of sequence b (one for a decode step, or
+ * a chunk of a prompt, appended before).  max_q: no sequence has more rows
+ * (rows beyond it are left out).  max_len: the longest sequence as far as the
+ * host knows; it sets how far the work is split, not what is read.
+ *   out  bf16 rows;  lse  device fp32 [total][q_heads], NULL = not wanted
+ * Rows past starts[batch] of out and lse are left as they are.  K codes enter
+ * the products exactly; rotated queries are held as two bf16 parts (2^-17);
+ * weights times value scales are rounded to bf16; sums and softmax statistics
+ * are fp32.  The workspace (jolt_cache_attention_workspace_size() bytes for the
+ * same sizes, 16-byte aligned) carries split rows from launch to launch: calls
+ * that may overlap (other streams, or replays of captured graphs) need one
+ * each. */
+jolt_status jolt_cache_attention_workspace_size(const jolt_cache *cache, int32_t batch, int32_t total, int32_t max_q,
+                                                int32_t max_len, int32_t q_heads, size_t *bytes);
+jolt_status jolt_cache_attention(jolt_handle h, const jolt_cache *cache, int32_t batch, const int32_t *starts,
+                                 int32_t total, int32_t max_q, int32_t max_len, int32_t q_heads, const jolt_rows *q,
+                                 const jolt_attn_terms *terms, const jolt_rows *out, float *lse, void *workspace,
+                                 size_t workspace_bytes, void *stream);
+
+/* The same for a tree of drafted tokens: the n <= 64 rows of sequence b are the
+ * drafted tokens at slots base .. base + n - 1 (base = lens[b] - n), appended
+ * before, and tree[row] (device uint64 [total]) has bit j set where the row
+ * sees slot j: its ancestors and itself.  Slot j stands at position
+ * base + popcount(tree of j) - 1, for distances and the window; a row sees
+ * every token before base that first, prefix and window leave it, and of the
+ * slots those of its mask within the window.  max_q is at most 64. */
+jolt_status jolt_tree_attention(jolt_handle h, const jolt_cache *cache, int32_t batch, const int32_t *starts,
+                                int32_t total, int32_t max_q, int32_t max_len, int32_t q_heads, const jolt_rows *q,
+                                const uint64_t *tree, const jolt_attn_terms *terms, const jolt_rows *out, float *lse,
+                                void *workspace, size_t workspace_bytes, void *stream);
+
 /* ---- factor export (device pointers into plan_ws) ------------------------ */
 /* After jolt_plan: where item i's factors live in plan_ws (fp32, device):
  *   ut    rt_max x T   row r = token-factor column r (descending eigenvalue)
@@ -325,7 +474,8 @@ size_t jolt_eigh_workspace_size(int32_t n, int32_t count, int32_t force_jacobi);
  * ("k_decode", "k_encode", "k_xm", "k_xtq", "k_eig_tridiag", "k_eig_trivec",
  * "k_eig_backtr", "k_eig_polish", "k_chol_inv",
  * "k_apply_linv", "k_gemm", "k_gram_rows", "k_reduce", "k_build_wt",
- * "k_jacobi_lds").  While a kernel's timer is on, each of its launches is
+ * "k_jacobi_lds", "k_cache_append", "k_cache_read", "k_cache_keep",
+ * "k_cache_attn", "k_cache_attn_join").  While a kernel's timer is on, each of its launches is
  * bracketed by a HIP event pair on its launch stream.  enable != 0 turns the
  * timer on and resets it; enable == 0 turns it off (the totals are kept).
  * Process-wide; h is used for error reporting only. */

@@ -6,8 +6,10 @@ the ctypes binding.
 """
 from .binding import (  # noqa: F401
     Jolt,
+    JoltCache,
     JoltError,
     jolt_alloc,
+    jolt_cache,
     jolt_config,
     jolt_item,
     make_config,

@@ -56,6 +56,23 @@ class jolt_factor_view(C.Structure):
                 ("rt_max", C.c_int32), ("rf_max", C.c_int32)]
 
 
+class jolt_cache(C.Structure):
+    _fields_ = [("H", C.c_int32), ("d", C.c_int32), ("bits", C.c_int32), ("page_tokens", C.c_int32),
+                ("pages", C.c_int32), ("max_pages", C.c_int32), ("rotate", C.c_int32), ("k_item_id", C.c_uint32),
+                ("v_item_id", C.c_uint32), ("reserved", C.c_uint32), ("seed", C.c_uint64), ("pool", C.c_void_p),
+                ("pool_bytes", C.c_uint64), ("table", C.c_void_p), ("lens", C.c_void_p)]
+
+
+class jolt_rows(C.Structure):
+    _fields_ = [("ptr", C.c_void_p), ("token_stride", C.c_int64), ("head_stride", C.c_int64)]
+
+
+class jolt_attn_terms(C.Structure):
+    _fields_ = [("scale", C.c_float), ("cap", C.c_float), ("window", C.c_int32), ("reserved", C.c_int32),
+                ("slopes", C.c_void_p), ("prefix", C.c_void_p), ("first", C.c_void_p), ("merge_out", C.c_void_p),
+                ("merge_lse", C.c_void_p)]
+
+
 EXPORTED = [
     "jolt_create", "jolt_destroy", "jolt_status_str", "jolt_last_error", "jolt_workspace_size",
     "jolt_item_bytes", "jolt_payload_size", "jolt_payload_layout", "jolt_payload_header",
@@ -63,7 +80,8 @@ EXPORTED = [
     "jolt_decompress", "jolt_decompress_noalloc", "jolt_attention_workspace_size", "jolt_decode_attention",
     "jolt_plan_factors", "jolt_plan_from_tables", "jolt_rotate", "jolt_quantize_pack",
     "jolt_unpack_dequant", "jolt_rademacher", "jolt_eigh", "jolt_eigh_workspace_size", "jolt_kernel_timer",
-    "jolt_kernel_time",
+    "jolt_kernel_time", "jolt_cache_pool_bytes", "jolt_cache_append", "jolt_cache_read", "jolt_cache_keep",
+    "jolt_cache_attention_workspace_size", "jolt_cache_attention", "jolt_tree_attention",
 ]
 
 _lib = None
@@ -117,6 +135,18 @@ def lib():
             "jolt_eigh_workspace_size": (SZ, [I32, I32, I32]),
             "jolt_kernel_timer": (I32, [P, C.c_char_p, I32]),
             "jolt_kernel_time": (I32, [P, C.c_char_p, C.POINTER(D), C.POINTER(I64)]),
+            "jolt_cache_pool_bytes": (I32, [C.POINTER(jolt_cache), C.POINTER(SZ)]),
+            "jolt_cache_append": (I32, [P, C.POINTER(jolt_cache), I32, P, I32, I32, I32, C.POINTER(jolt_rows),
+                                        C.POINTER(jolt_rows), P]),
+            "jolt_cache_read": (I32, [P, C.POINTER(jolt_cache), I32, P, P, I32, I32, I32, C.POINTER(jolt_rows),
+                                      C.POINTER(jolt_rows), P]),
+            "jolt_cache_keep": (I32, [P, C.POINTER(jolt_cache), I32, P, P, P, I32, P]),
+            "jolt_cache_attention_workspace_size": (I32, [C.POINTER(jolt_cache), I32, I32, I32, I32, I32,
+                                                          C.POINTER(SZ)]),
+            "jolt_cache_attention": (I32, [P, C.POINTER(jolt_cache), I32, P, I32, I32, I32, I32, C.POINTER(jolt_rows),
+                                           C.POINTER(jolt_attn_terms), C.POINTER(jolt_rows), P, P, SZ, P]),
+            "jolt_tree_attention": (I32, [P, C.POINTER(jolt_cache), I32, P, I32, I32, I32, I32, C.POINTER(jolt_rows),
+                                          P, C.POINTER(jolt_attn_terms), C.POINTER(jolt_rows), P, P, SZ, P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -313,6 +343,45 @@ def jolt_kernel_time(h, kernel: str):
     return ms.value, n.value
 
 
+def jolt_cache_pool_bytes(cache: jolt_cache) -> int:
+    b = C.c_size_t()
+    _check(lib().jolt_cache_pool_bytes(C.byref(cache), C.byref(b)))
+    return b.value
+
+
+def jolt_cache_append(h, cache: jolt_cache, batch, starts_ptr, total, max_new, dtype, k: jolt_rows, v: jolt_rows,
+                      stream):
+    _check(lib().jolt_cache_append(h, cache, batch, starts_ptr, total, max_new, dtype, k, v, stream), h)
+
+
+def jolt_cache_read(h, cache: jolt_cache, batch, first_ptr, starts_ptr, total, max_rows, dtype, k: jolt_rows,
+                    v: jolt_rows, stream):
+    _check(lib().jolt_cache_read(h, cache, batch, first_ptr, starts_ptr, total, max_rows, dtype, k, v, stream), h)
+
+
+def jolt_cache_keep(h, cache: jolt_cache, batch, base_ptr, starts_ptr, path_ptr, total, stream):
+    _check(lib().jolt_cache_keep(h, cache, batch, base_ptr, starts_ptr, path_ptr, total, stream), h)
+
+
+def jolt_cache_attention_workspace_size(cache: jolt_cache, batch, total, max_q, max_len, q_heads) -> int:
+    b = C.c_size_t()
+    _check(lib().jolt_cache_attention_workspace_size(C.byref(cache), batch, total, max_q, max_len, q_heads,
+                                                     C.byref(b)))
+    return b.value
+
+
+def jolt_cache_attention(h, cache: jolt_cache, batch, starts_ptr, total, max_q, max_len, q_heads, q: jolt_rows,
+                         terms: jolt_attn_terms, out: jolt_rows, lse_ptr, ws_ptr, ws_bytes, stream):
+    _check(lib().jolt_cache_attention(h, cache, batch, starts_ptr, total, max_q, max_len, q_heads, q, terms, out,
+                                      lse_ptr, ws_ptr, ws_bytes, stream), h)
+
+
+def jolt_tree_attention(h, cache: jolt_cache, batch, starts_ptr, total, max_q, max_len, q_heads, q: jolt_rows,
+                        tree_ptr, terms: jolt_attn_terms, out: jolt_rows, lse_ptr, ws_ptr, ws_bytes, stream):
+    _check(lib().jolt_tree_attention(h, cache, batch, starts_ptr, total, max_q, max_len, q_heads, q, tree_ptr, terms,
+                                     out, lse_ptr, ws_ptr, ws_bytes, stream), h)
+
+
 # ------------------------------------------------------------------ helpers
 def make_item(L, H, T, d, dtype="bf16", item_id=0, seed=0) -> jolt_item:
     return jolt_item(L, H, T, d, JOLT_F32 if dtype == "f32" else JOLT_BF16, item_id, seed)
@@ -400,6 +469,159 @@ class Jolt:
 
     def factors(self, i: int) -> jolt_factor_view:
         return jolt_plan_factors(self.cfg, self.items, self.plan_ws.data_ptr(), i)
+
+    def close(self):
+        if self.h is not None:
+            jolt_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class JoltCache:
+    """The token cache of one layer: the tokens after a compressed prefill.
+
+    Holds a handle, the caller's pool (uint8), page table (int32 [batch,
+    max_pages]) and lengths (int32 [batch]), and a workspace for split
+    attention rows for each stream that calls come on.  The tensors stay the
+    caller's: update `lens` (and `table`) in place between calls; rows of a
+    call count as the last tokens of their sequence.  Calls go to the current
+    stream of the cache's device.  Captured graphs that may be replayed side by
+    side pass a `workspace` of their own each (uint8, at least
+    workspace_bytes(...) long).
+    """
+
+    def __init__(self, H, d, bits, pool, table, lens, page_tokens=64, rotate=True, seed=0, k_item_id=0, v_item_id=1):
+        import torch
+        self.torch = torch
+        self.h = None
+        self.device = pool.device
+        for name, t, dt, dims in (("pool", pool, torch.uint8, None), ("table", table, torch.int32, 2),
+                                  ("lens", lens, torch.int32, 1)):
+            self._tensor(name, t, dt, dims)
+        if table.shape[0] != lens.shape[0]:
+            raise ValueError("table and lens differ in their number of sequences")
+        c = jolt_cache(H, d, bits, page_tokens, 0, table.shape[1], int(bool(rotate)), k_item_id, v_item_id, 0, seed,
+                       pool.data_ptr(), pool.numel(), table.data_ptr(), lens.data_ptr())
+        c.pages = 1
+        self.page_bytes = jolt_cache_pool_bytes(c)
+        c.pages = pool.numel() // self.page_bytes
+        self.c, self.pool, self.table, self.lens = c, pool, table, lens
+        self.batch, self.H, self.d = int(lens.shape[0]), H, d
+        self.workspaces = {}          # stream -> every workspace it has used, the last one the largest
+        with torch.cuda.device(self.device):
+            self.h = jolt_create(self.device.index)
+
+    def _tensor(self, name, t, dtype, dims=None):
+        if t.dtype != dtype or t.device != self.device or not t.is_contiguous() or \
+                (dims is not None and t.dim() != dims):
+            raise ValueError("%s must be a contiguous %s tensor%s on %s"
+                             % (name, dtype, "" if dims is None else " of %d dimensions" % dims, self.device))
+        return t.data_ptr()
+
+    def _starts(self, starts):
+        if starts.numel() != self.batch + 1:
+            raise ValueError("starts must have batch + 1 entries")
+        return self._tensor("starts", starts, self.torch.int32)
+
+    def _rows(self, name, t, heads, dtypes):
+        if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != self.d or t.dtype not in dtypes \
+                or t.device != self.device or (t.stride(2) != 1 and t.numel()):
+            raise ValueError("%s must be [rows, %d, %d] with contiguous features, of %s, on %s"
+                             % (name, heads, self.d, " or ".join(map(str, dtypes)), self.device))
+        return jolt_rows(t.data_ptr(), t.stride(0), t.stride(1))
+
+    def _kv(self, k, v):
+        dt = (self.torch.bfloat16, self.torch.float32)
+        rk, rv = self._rows("k", k, self.H, dt), self._rows("v", v, self.H, dt)
+        if k.dtype != v.dtype or k.shape[0] != v.shape[0]:
+            raise ValueError("k and v differ in dtype or rows")
+        return rk, rv, JOLT_F32 if k.dtype == self.torch.float32 else JOLT_BF16
+
+    def _stream(self):
+        return self.torch.cuda.current_stream(self.device).cuda_stream
+
+    def append(self, k, v, starts, max_new):
+        """Write rows k, v [total, H, d] (bf16 or fp32) as the last tokens of their sequences."""
+        rk, rv, dt = self._kv(k, v)
+        jolt_cache_append(self.h, self.c, self.batch, self._starts(starts), k.shape[0], max_new, dt, rk, rv,
+                          self._stream())
+
+    def read(self, first, starts, max_rows, k, v):
+        """Read tokens first[b] .. of every sequence into k, v [total, H, d] (bf16 or fp32)."""
+        rk, rv, dt = self._kv(k, v)
+        if first is not None and first.numel() != self.batch:
+            raise ValueError("first must have batch entries")
+        fp = None if first is None else self._tensor("first", first, self.torch.int32)
+        jolt_cache_read(self.h, self.c, self.batch, fp, self._starts(starts), k.shape[0], max_rows, dt, rk, rv,
+                        self._stream())
+
+    def keep(self, base, starts, path):
+        """Move drafted tokens base[b] + path[i] of every sequence to base[b] + 0, 1, ..."""
+        if base.numel() != self.batch:
+            raise ValueError("base must have batch entries")
+        jolt_cache_keep(self.h, self.c, self.batch, self._tensor("base", base, self.torch.int32), self._starts(starts),
+                        self._tensor("path", path, self.torch.int32), path.numel(), self._stream())
+
+    def workspace_bytes(self, total, max_q, max_len, q_heads) -> int:
+        return jolt_cache_attention_workspace_size(self.c, self.batch, total, max_q, max_len, q_heads)
+
+    def _attend(self, q, starts, max_q, max_len, tree, out, lse, scale, cap, slopes, window, prefix, first, merge_out,
+                merge_lse, workspace):
+        torch = self.torch
+        total, hq = q.shape[0], q.shape[1]
+        rq, ro = self._rows("q", q, hq, (torch.bfloat16,)), self._rows("out", out, hq, (torch.bfloat16,))
+        if out.shape[0] != total:
+            raise ValueError("q and out differ in rows")
+        t = jolt_attn_terms(scale, cap, window, 0)
+        f32, i32 = torch.float32, torch.int32
+        for name, x, dt, numel in (("slopes", slopes, f32, hq), ("prefix", prefix, i32, self.batch),
+                                   ("first", first, i32, total), ("merge_out", merge_out, f32, total * hq * self.d),
+                                   ("merge_lse", merge_lse, f32, total * hq)):
+            if x is not None:
+                if x.numel() != numel:
+                    raise ValueError("%s must have %d entries" % (name, numel))
+                setattr(t, name, self._tensor(name, x, dt))
+        if lse is not None and lse.numel() != total * hq:
+            raise ValueError("lse must be [rows, q_heads]")
+        lp = None if lse is None else self._tensor("lse", lse, f32)
+        need = self.workspace_bytes(total, max_q, max_len, hq)
+        stream = self._stream()
+        if workspace is None:
+            if need:
+                # none is dropped: a captured graph goes on using the one it was captured with
+                have = self.workspaces.setdefault(stream, [])
+                if not have or have[-1].numel() < need:
+                    have.append(torch.empty(need, dtype=torch.uint8, device=self.device))
+                workspace = have[-1]
+        elif workspace.device != self.device or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous uint8 tensor on %s" % (self.device,))
+        wp, wb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+        sp = self._starts(starts)
+        if tree is None:
+            jolt_cache_attention(self.h, self.c, self.batch, sp, total, max_q, max_len, hq, rq, t, ro, lp, wp, wb,
+                                 stream)
+        else:
+            if tree.numel() != total:
+                raise ValueError("tree must have one mask for each row")
+            jolt_tree_attention(self.h, self.c, self.batch, sp, total, max_q, max_len, hq, rq,
+                                self._tensor("tree", tree, torch.int64), t, ro, lp, wp, wb, stream)
+
+    def attention(self, q, starts, max_q, max_len, out, lse=None, scale=None, cap=0.0, slopes=None, window=0,
+                  prefix=None, first=None, merge_out=None, merge_lse=None, workspace=None):
+        """Attention of q [total, q_heads, d] (bf16) over the cache into out (bf16) and lse (fp32)."""
+        self._attend(q, starts, max_q, max_len, None, out, lse, self.d ** -0.5 if scale is None else scale, cap,
+                     slopes, window, prefix, first, merge_out, merge_lse, workspace)
+
+    def tree_attention(self, q, starts, max_q, max_len, tree, out, lse=None, scale=None, cap=0.0, slopes=None,
+                       window=0, prefix=None, first=None, merge_out=None, merge_lse=None, workspace=None):
+        """The same for drafted tokens: tree (int64 bit masks, one a row) says which slots a row sees."""
+        self._attend(q, starts, max_q, max_len, tree, out, lse, self.d ** -0.5 if scale is None else scale, cap,
+                     slopes, window, prefix, first, merge_out, merge_lse, workspace)
 
     def close(self):
         if self.h is not None:

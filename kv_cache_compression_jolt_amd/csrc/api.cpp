@@ -79,6 +79,8 @@ void clear_err(jolt_handle h) {
     if (h) h->err.clear();
 }
 
+int handle_device(jolt_handle h) { return h->device; }
+
 DualTables &dual_tables(jolt_handle h) { return h->dual; }
 
 hipError_t readback_buffer(jolt_handle h, size_t bytes, uint8_t **buf) {

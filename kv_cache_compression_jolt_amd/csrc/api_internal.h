@@ -16,6 +16,7 @@ namespace jolt {
 jolt_status fail(jolt_handle h, jolt_status s, const char *fmt, ...);
 jolt_status hip_fail(jolt_handle h, hipError_t e, const char *where);
 void clear_err(jolt_handle h);
+int handle_device(jolt_handle h);
 // The dual's candidate grid and per-shape byte-ordered candidates depend only
 // on the configuration and the item shapes; a handle keeps the last ones from
 // one plan to the next.

@@ -1,0 +1,93 @@
+// Token cache: argument checks and sizes.  Plain C++ (no HIP), so that the
+// checks also build and run on their own on the host.
+#include "cache.h"
+
+#include <algorithm>
+#include <limits>
+
+namespace jolt {
+
+int page_shift_of(int page_tokens) {
+    for (int s = 5; s <= 8; ++s)
+        if (page_tokens == (1 << s)) return s;
+    return -1;
+}
+
+static jolt_status refuse(const char **msg, jolt_status s, const char *text) {
+    if (msg) *msg = text;
+    return s;
+}
+
+jolt_status cache_check(const jolt_cache *c, int32_t batch, const char **msg) {
+    if (!c) return refuse(msg, JOLT_E_INVALID, "cache: NULL");
+    if (c->d != 64 && c->d != 128) return refuse(msg, JOLT_E_UNSUPPORTED, "cache: d must be 64 or 128");
+    if (c->bits != 4 && c->bits != 8) return refuse(msg, JOLT_E_UNSUPPORTED, "cache: bits must be 4 or 8");
+    if (page_shift_of(c->page_tokens) < 0)
+        return refuse(msg, JOLT_E_UNSUPPORTED, "cache: page_tokens must be 32, 64, 128 or 256");
+    if (c->H < 1 || c->H > 65535) return refuse(msg, JOLT_E_INVALID, "cache: H must be 1..65535");
+    if (c->pages < 0 || c->max_pages < 0) return refuse(msg, JOLT_E_INVALID, "cache: negative page count");
+    if ((int64_t)c->max_pages * c->page_tokens > std::numeric_limits<int32_t>::max() / 2)
+        return refuse(msg, JOLT_E_UNSUPPORTED, "cache: more than 2^30 tokens in a sequence");
+    if (batch < 0 || batch > (1 << 20)) return refuse(msg, JOLT_E_INVALID, "cache: batch must be 0..2^20");
+    if (batch > 0) {
+        if (!c->lens || (c->max_pages > 0 && !c->table)) return refuse(msg, JOLT_E_INVALID, "cache: NULL table or lens");
+        if (c->pages > 0 && !c->pool) return refuse(msg, JOLT_E_INVALID, "cache: NULL pool");
+        if (reinterpret_cast<uintptr_t>(c->pool) % 16)
+            return refuse(msg, JOLT_E_INVALID, "cache: the pool must be 16-byte aligned");
+        const uint64_t page = (uint64_t)page_layout(c->page_tokens, c->d, c->bits).bytes * c->H;
+        if (c->pool_bytes / page < (uint64_t)c->pages) return refuse(msg, JOLT_E_WORKSPACE, "cache: pool smaller than its pages");
+    }
+    return JOLT_OK;
+}
+
+// Row views: 16-byte aligned rows; an output's rows must not overlap (token- or
+// head-major, or padded forms of these).
+jolt_status rows_check(const jolt_rows *r, int64_t total, int heads, int d, int elem, bool output, const char **msg) {
+    if (total == 0) return JOLT_OK;
+    if (!r || !r->ptr) return refuse(msg, JOLT_E_INVALID, "rows: NULL");
+    const int64_t unit = 16 / elem;
+    if (reinterpret_cast<uintptr_t>(r->ptr) % 16 || r->token_stride % unit || r->head_stride % unit)
+        return refuse(msg, JOLT_E_INVALID, "rows: pointer and strides must be multiples of 16 bytes");
+    if (r->token_stride < 0 || r->head_stride < 0) return refuse(msg, JOLT_E_INVALID, "rows: negative stride");
+    const int64_t lim = std::numeric_limits<int64_t>::max() / 16 / std::max<int64_t>(std::max<int64_t>(total, heads), 1);
+    if (r->token_stride > lim || r->head_stride > lim) return refuse(msg, JOLT_E_INVALID, "rows: stride too large");
+    if (output) {
+        const int64_t ts = r->token_stride, hs = r->head_stride;
+        const bool token_major = (total == 1 || ts >= (heads - 1) * hs + d) && (heads == 1 || hs >= d);
+        const bool head_major = (heads == 1 || hs >= (total - 1) * ts + d) && (total == 1 || ts >= d);
+        if (!token_major && !head_major) return refuse(msg, JOLT_E_INVALID, "rows: output rows overlap");
+    }
+    return JOLT_OK;
+}
+
+jolt_status cache_attn_check(const jolt_cache *c, int32_t batch, int32_t total, int32_t max_q, int32_t max_len,
+                             int32_t q_heads, const char **msg) {
+    jolt_status s = cache_check(c, batch, msg);
+    if (s) return s;
+    if (total < 0 || max_q < 0 || max_len < 0) return refuse(msg, JOLT_E_INVALID, "attention: negative size");
+    if (q_heads < c->H || q_heads % c->H || q_heads > 65535)
+        return refuse(msg, JOLT_E_INVALID, "attention: q_heads must be a multiple of H, at most 65535");
+    const int64_t tiles = (int64_t)batch * c->H * (((int64_t)max_q * (q_heads / c->H) + 15) / 16);
+    if (tiles > (1 << 24) || (int64_t)total * q_heads > std::numeric_limits<int32_t>::max() / 2)
+        return refuse(msg, JOLT_E_UNSUPPORTED, "attention: too many query rows for one call");
+    return JOLT_OK;
+}
+
+// Token ranges: enough workgroups for the 256 CUs (about four each), none of
+// fewer than 256 tokens.
+AttnPlan cache_attn_plan(const jolt_cache &c, int batch, int64_t total, int max_q, int max_len, int q_heads) {
+    AttnPlan p{};
+    const int64_t G = q_heads / c.H;
+    const int64_t tiles = std::max<int64_t>(1, (int64_t)batch * c.H * (((int64_t)max_q * G + 15) / 16));
+    const int64_t by_len = std::max<int64_t>(1, max_len / 256);
+    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(by_len, 1024 / tiles));
+    if (p.splits > 1) {
+        const size_t rows = (size_t)total * q_heads;
+        p.ml_off = 0;
+        p.part_off = (p.splits * rows * 2 * 4 + 255) / 256 * 256;
+        p.bytes = p.part_off + p.splits * rows * c.d * 4;
+    }
+    return p;
+}
+
+}  // namespace jolt

@@ -1,0 +1,559 @@
+// Attention over the token cache (jolt_cache_attention, jolt_tree_attention).
+//
+// For a query row q of KV head h, with u the stored codes (unsigned, offset
+// c0), sc_g the scale of group g of 64 features and q' the query in the cache's
+// domain (rotated: q' = (1/sqrt d) H (s o q)):
+//   q . k_t = sum_g sc_g[t] (sum_{f in g} q'_f u_f[t] - c0 sum_{f in g} q'_f)
+//   o'_f    = sum_t w_g[t] u_f[t] - c0 sum_t w_g[t],   w_g[t] = p_t sc_g^V[t]
+// and o = o' / sum p, rotated back once per row.  So the codes go into the
+// matrix cores as they are stored, as integers, exact in bf16; the offset is
+// the accumulator's initial value for the scores and one extra product with a
+// row of ones for the values; scales are applied to scores and weights in fp32.
+// A 4-bit code becomes bf16 by or-ing it under the exponent of 128 (value
+// 128 + u, c0 = 136), two codes per and-or.
+//
+// Products are S^T = K Q^T and O^T = V^T P^T (16x16x32): a lane then holds one
+// query column and 8 tokens' scores, in exactly the order that the second
+// product takes its P^T operand in, so weights never leave registers.  Softmax
+// runs in one pass with a running maximum per column, which is raised, and the
+// sums rescaled, only when a score passes it by 2^8.
+#include <algorithm>
+
+#include "cache.h"
+#include "cache_dev.h"
+#include "jolt_internal.h"
+#include "ktimer.h"
+
+namespace jolt {
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kCols = 16;                 // query columns of a tile
+constexpr int kWaves = 4;
+
+__device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
+
+__device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// a unit of 8 codes as bf16 (4 bits: 128 + code, 8 bits: code)
+template <int BITS>
+__device__ __forceinline__ bf16x8 unit_bf16(const uint32_t *w) {
+    uint32_t r[4];
+    if constexpr (BITS == 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] = ((w[0] >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t v = w[i >> 1] >> (16 * (i & 1));
+            const uint32_t lo = __float_as_uint((float)(v & 255u)), hi = __float_as_uint((float)((v >> 8) & 255u));
+            r[i] = __builtin_amdgcn_perm(hi, lo, 0x07060302u);       // the upper halves: integers < 256 fit bf16
+        }
+    }
+    const uint4 q = make_uint4(r[0], r[1], r[2], r[3]);
+    return __builtin_bit_cast(bf16x8, q);
+}
+template <int BITS> constexpr float code_offset() { return BITS == 4 ? 136.f : 128.f; }
+
+// N dwords from a 16-byte (N = 4, 8, ...) or 8-byte (N = 2) aligned address
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[N]) {
+    if constexpr (N == 2) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        w[0] = v.x; w[1] = v.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(p + 4 * i);
+            w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
+        }
+    }
+}
+__device__ __forceinline__ float scale_of(const uint32_t *w, int e) {
+    return __uint_as_float((e & 1) ? (w[e >> 1] & 0xFFFF0000u) : (w[e >> 1] << 16));
+}
+
+// One wave's share of a 32-token block as it lies in memory
+template <int D, int BITS>
+struct BlockRegs {
+    static constexpr int kU = BITS / 4;                 // dwords of a unit
+    static constexpr int kK = D / 32 * kU;              // K dwords of a lane and subtile
+    static constexpr int kV = D / 16 * kU;              // V dwords of a lane
+    uint32_t k[2][kK], v[kV], ks[D / 64][4], vs[D / 64][4];
+
+    // tokens t0 .. t0 + 31, inside one page; lane (m, g): K chunk g of token
+    // rows 8 (m/4) + 4 u + m%4, V units of tokens 8 g .. 8 g + 7, and those
+    // tokens' scales
+    __device__ __forceinline__ void load(const uint8_t *blk, const PageLayout &pl, int P, int tin, int m, int g) {
+        constexpr int rowb = D * BITS / 8;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            load_words<kK>(blk + (tin + 8 * (m >> 2) + 4 * u + (m & 3)) * rowb + g * (rowb / 4), k[u]);
+        const uint8_t *vp = blk + pl.v_codes + ((tin >> 3) + g) * (D * BITS);
+#pragma unroll
+        for (int i = 0; i < kV; i += 4) {
+            uint32_t t[4];
+            load_words<4>(vp + i * 64 + m * 16, t);     // 16 lanes x 16 bytes per step
+#pragma unroll
+            for (int x = 0; x < 4; ++x) v[i + x] = t[x];
+        }
+#pragma unroll
+        for (int q = 0; q < D / 64; ++q) {
+            load_words<4>(blk + pl.k_scales + (q * P + tin + 8 * g) * 2, ks[q]);
+            load_words<4>(blk + pl.v_scales + (q * P + tin + 8 * g) * 2, vs[q]);
+        }
+    }
+};
+// the feature that row m of value tile i stands for (the order of the 16-byte loads)
+template <int BITS>
+__device__ __forceinline__ constexpr int value_feature(int i, int m) {
+    constexpr int per = 16 / BITS;                      // units (features) of a 16-byte load
+    return (i / per) * (16 * per) + m * per + i % per;
+}
+
+// Query column state: what a row may see, in tokens
+struct Column {
+    int pos, low, first, hi;              // t >= first, and (t < prefix or low <= t < hi)
+    float slope;                          // slope * log2 e
+    uint64_t mask;                        // tree: visible slots
+};
+
+// out row: o (8 features of lane j of D/8), l and m (log2 domain) of the whole row
+template <int D, bool ROT>
+__device__ __forceinline__ void finish_row(const CacheAttnArgs &a, int64_t row, int head, int j, float (&o)[8], float m,
+                                           float l, bool store) {
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] *= inv;
+    if constexpr (ROT) {
+        fwht_row<D>(o, j);
+        const uint32_t sb = sign_byte(a.c.sv, j);
+        const float isd = D == 128 ? 0.08838834764831845f : 0.125f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = flip(o[e] * isd, (sb >> e) & 1);
+    }
+    if (!store) return;
+    float lse = l == 0.f ? neg_inf() : (m + __builtin_amdgcn_logf(l)) * kLn2;
+    const int64_t at = row * a.hq + head;
+    if (a.merge_out) {
+        const float l2 = a.merge_lse[at], mx = fmaxf(lse, l2);
+        const float w1 = mx == neg_inf() ? 0.f : __builtin_amdgcn_exp2f((lse - mx) * kLog2e);
+        const float w2 = mx == neg_inf() ? 0.f : __builtin_amdgcn_exp2f((l2 - mx) * kLog2e);
+        const float s = w1 + w2, is = s == 0.f ? 0.f : 1.f / s;
+        const float4 *p = reinterpret_cast<const float4 *>(a.merge_out + at * D + 8 * j);
+        const float4 x = p[0], y = p[1];
+        const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {                   // a part that saw nothing adds nothing, whatever its rows hold
+            const float p1 = w1 == 0.f ? 0.f : o[e] * w1, p2 = w2 == 0.f ? 0.f : v[e] * w2;
+            o[e] = (p1 + p2) * is;
+        }
+        lse = s == 0.f ? neg_inf() : mx + __builtin_amdgcn_logf(s) * kLn2;
+    }
+    uint16_t *dst = static_cast<uint16_t *>(a.out.ptr) + row * a.out.ts + head * a.out.hs + 8 * j;
+    *reinterpret_cast<uint4 *>(dst) =
+        make_uint4(bf16_pair(o[0], o[1]), bf16_pair(o[2], o[3]), bf16_pair(o[4], o[5]), bf16_pair(o[6], o[7]));
+    if (a.lse && j == 0) a.lse[at] = lse;
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------- attention
+// One workgroup of 4 waves per (token range, KV head, tile of 16 query columns,
+// sequence); column c of a sequence's KV head is query row c / G, head h G +
+// c % G.  The waves take the range's 32-token blocks in turn (each block's
+// fragments go from memory to registers, the next block's while this one is
+// computed) and join their sums through LDS at the end.
+template <int D, int BITS, bool ROT>
+__global__ __launch_bounds__(64 * kWaves) void k_cache_attn(CacheAttnArgs a, int ctiles) {
+    constexpr int NK = D / 32, NV = D / 16, NG = D / 64, KU = BITS / 4;
+    int64_t w = blockIdx.x;
+    const int split = (int)(w % a.splits);
+    w /= a.splits;
+    const int ct = (int)(w % ctiles);
+    w /= ctiles;
+    const int h = (int)(w % a.c.H), b = (int)(w / a.c.H);
+    int s0;
+    const int nall = ragged_rows(a.starts, b, a.total, &s0), n = min(nall, a.max_q);
+    if (ct * kCols >= n * a.G) return;
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, m = lane & 15, g = lane >> 4;
+    const int len = cache_len(a.c, b), base = a.c.lens[b] - nall;
+    const int prefix = a.prefix ? a.prefix[b] : 0;
+
+    __shared__ __align__(16) float sm[kWaves * kCols * (D + 4)];
+    __shared__ float sml[2][kWaves][kCols];
+
+    // ---- the queries in the cache's domain, one row per D / 8 lanes, through LDS
+    {
+        const int r = tid / (D / 8), j = tid % (D / 8);
+        if (D == 128 || tid < 128) {
+            const int c = ct * kCols + r;
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = 0.f;
+            if (c < n * a.G) {
+                const int i = c / a.G, hd = h * a.G + c % a.G;
+                const uint4 v = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q.ptr) +
+                                                                 (int64_t)(s0 + i) * a.q.ts + hd * a.q.hs + 8 * j);
+                const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = scale_of(q, e);
+            }
+            if constexpr (ROT) {
+                const uint32_t sb = sign_byte(a.c.sk, j);
+                const float isd = D == 128 ? 0.08838834764831845f : 0.125f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = flip(x[e], (sb >> e) & 1);
+                fwht_row<D>(x, j);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] *= isd;
+            }
+            float4 *p = reinterpret_cast<float4 *>(sm + r * (D + 4) + 8 * j);
+            p[0] = make_float4(x[0], x[1], x[2], x[3]);
+            p[1] = make_float4(x[4], x[5], x[6], x[7]);
+        }
+    }
+    __syncthreads();
+    // fragments: column m, features 32 k + 8 g + e; hi and (rotated) lo parts;
+    // cinit: minus the offset times the column's sum over each group
+    constexpr int NP = ROT ? 2 : 1;
+    bf16x8 qf[NP][NK];
+    float cinit[NG];
+#pragma unroll
+    for (int q = 0; q < NG; ++q) cinit[q] = 0.f;
+#pragma unroll
+    for (int k = 0; k < NK; ++k) {
+        const float *p = sm + m * (D + 4) + 32 * k + 8 * g;
+        float sum = 0.f;
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float x0 = p[2 * i], x1 = p[2 * i + 1];
+            hi[i] = bf16_pair(x0, x1);
+            const float h0 = __uint_as_float(hi[i] << 16), h1 = __uint_as_float(hi[i] & 0xFFFF0000u);
+            sum += h0 + h1;
+            if constexpr (ROT) {
+                lo[i] = bf16_pair(x0 - h0, x1 - h1);
+                sum += __uint_as_float(lo[i] << 16) + __uint_as_float(lo[i] & 0xFFFF0000u);
+            }
+        }
+        qf[0][k] = __builtin_bit_cast(bf16x8, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+        if constexpr (ROT) qf[NP - 1][k] = __builtin_bit_cast(bf16x8, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+        cinit[k / 2] += sum;
+    }
+#pragma unroll
+    for (int q = 0; q < NG; ++q) {
+        cinit[q] += __shfl_xor(cinit[q], 16);
+        cinit[q] += __shfl_xor(cinit[q], 32);
+        cinit[q] *= -code_offset<BITS>();
+    }
+    __syncthreads();                                    // sm is reused by the join
+
+    // ---- what the columns see
+    const int c = ct * kCols + m, ncol = n * a.G;
+    const bool cv = c < ncol;
+    Column col;
+    {
+        const int i = cv ? c / a.G : 0;
+        col.mask = 0;
+        col.pos = base + i;
+        if (a.tree) {
+            col.mask = cv ? a.tree[s0 + i] : 0;
+            col.pos = base + max(__popcll(col.mask) - 1, 0);
+        }
+        col.first = cv && a.first ? a.first[s0 + i] : 0;
+        col.low = a.window > 0 ? col.pos - a.window + 1 : -0x7FFFFFFF;
+        col.hi = a.tree ? base : col.pos + 1;
+        col.slope = a.slopes ? a.slopes[h * a.G + (cv ? c % a.G : 0)] * kLog2e : 0.f;
+    }
+    // tokens any column may see [lo_any, hi_any) apart from the prefix, and those
+    // all columns see [lo_all, hi_all)
+    int lo_any = cv ? max(col.low, col.first) : 0x7FFFFFFF, hi_any = cv ? col.hi : 0;
+    int lo_all = cv ? max(col.low, col.first) : -0x7FFFFFFF, hi_all = cv ? col.hi : 0x7FFFFFFF;
+    int first_any = cv ? col.first : 0x7FFFFFFF;
+#pragma unroll
+    for (int x = 1; x < 16; x *= 2) {
+        lo_any = min(lo_any, __shfl_xor(lo_any, x));
+        hi_any = max(hi_any, __shfl_xor(hi_any, x));
+        lo_all = max(lo_all, __shfl_xor(lo_all, x));
+        hi_all = min(hi_all, __shfl_xor(hi_all, x));
+        first_any = min(first_any, __shfl_xor(first_any, x));
+    }
+    if (a.tree) hi_any = len;
+    hi_any = min(max(hi_any, prefix), len);
+    hi_all = min(hi_all, len);
+    const int begin = max(prefix > first_any ? min(first_any, lo_any) : lo_any, 0);
+
+    // ---- this workgroup's blocks, this wave's every kWaves-th
+    const int blk0 = begin >> 5, nblk = hi_any > begin ? ((hi_any + 31) >> 5) - blk0 : 0;
+    const int per = (nblk + a.splits - 1) / a.splits;
+    const int bs = blk0 + split * per, be = min(bs + per, blk0 + nblk);
+
+    const int P = 1 << a.c.page_shift;
+    const PageLayout pl = page_layout(P, D, BITS);
+    f32x4 acc[NV], corr[NG];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int q = 0; q < NG; ++q) corr[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float mrun = neg_inf(), lrun = 0.f;
+    const float mul = a.scale * kLog2e, cap_mul = a.cap > 0.f ? a.scale / a.cap * (2.f * kLog2e) : 0.f;
+    const bf16x8 ones = __builtin_bit_cast(bf16x8, make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u));
+
+    auto page_of = [&](int blk) -> int {                // -1: nothing to do there
+        if (blk >= be) return -1;
+        const int t0 = blk << 5;
+        if (t0 >= prefix && t0 + 32 <= lo_any) return -1;
+        return cache_page(a.c, b, t0);
+    };
+    BlockRegs<D, BITS> cur, nxt;
+    int blk = bs + wave, page = page_of(blk);
+    if (page >= 0) cur.load(a.c.pool + cache_block_offset(a.c, page, h), pl, P, (blk << 5) & (P - 1), m, g);
+    for (; blk < be; blk += kWaves) {
+        const int pnext = page_of(blk + kWaves);
+        if (pnext >= 0)
+            nxt.load(a.c.pool + cache_block_offset(a.c, pnext, h), pl, P, ((blk + kWaves) << 5) & (P - 1), m, g);
+        if (page >= 0) {
+            const int t0 = blk << 5;
+            // scores: lane (column m) has tokens t0 + 8 g + e
+            float s[8];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                for (int q = 0; q < NG; ++q) {
+                    f32x4 x = {cinit[q], cinit[q], cinit[q], cinit[q]};
+#pragma unroll
+                    for (int k = 2 * q; k < 2 * q + 2; ++k) {
+                        const bf16x8 kf = unit_bf16<BITS>(&cur.k[u][k * KU]);
+#pragma unroll
+                        for (int p = 0; p < NP; ++p) x = mfma16(kf, qf[p][k], x);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float ks = scale_of(cur.ks[q], 4 * u + i);
+                        s[4 * u + i] = q == 0 ? x[i] * ks : fmaf(x[i], ks, s[4 * u + i]);
+                    }
+                }
+            }
+            if (a.cap > 0.f) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {           // tanh |y| = (1 - x) / (1 + x), x = exp(-2 |y|)
+                    const float x = __builtin_amdgcn_exp2f(-fabsf(s[e] * cap_mul));
+                    s[e] = copysignf((1.f - x) * __builtin_amdgcn_rcpf(1.f + x), s[e]) * (a.cap * kLog2e);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s[e] *= mul;
+            }
+            const bool full = t0 >= lo_all && t0 + 32 <= hi_all;
+            uint32_t vis = 0xFFu;
+            if (!full || a.slopes) {
+                vis = 0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int t = t0 + 8 * g + e;
+                    int tp = t;
+                    bool v;
+                    if (a.tree && t >= base) {
+                        const int slot = t - base;
+                        const bool in = slot < n && slot < kMaxKeep && t < len;
+                        tp = base + (in ? max(__popcll(a.tree[s0 + slot]) - 1, 0) : 0);
+                        v = in && ((col.mask >> (slot & 63)) & 1) && tp >= col.low;
+                    } else {
+                        v = t < len && t >= col.first && (t < prefix || (t >= col.low && t < col.hi));
+                    }
+                    vis |= (uint32_t)v << e;
+                    s[e] -= col.slope * fabsf((float)(col.pos - tp));
+                    s[e] = v ? s[e] : neg_inf();
+                }
+            }
+            float mx = s[0];
+#pragma unroll
+            for (int e = 1; e < 8; ++e) mx = fmaxf(mx, s[e]);
+            if (__any(mx > mrun + 8.f)) {
+                mx = fmaxf(mx, __shfl_xor(mx, 16));
+                mx = fmaxf(mx, __shfl_xor(mx, 32));
+                mx = fmaxf(mx, mrun);
+                const float alpha = mx == mrun ? 1.f : __builtin_amdgcn_exp2f(mrun - mx);
+                mrun = mx;
+                lrun *= alpha;
+#pragma unroll
+                for (int i = 0; i < NV; ++i) acc[i] *= alpha;
+#pragma unroll
+                for (int q = 0; q < NG; ++q) corr[q] *= alpha;
+            }
+            const float mu = mrun == neg_inf() ? 0.f : mrun;
+            float p[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                p[e] = __builtin_amdgcn_exp2f(s[e] - mu);
+                lrun += p[e];
+            }
+#pragma unroll
+            for (int q = 0; q < NG; ++q) {
+                uint32_t wv[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float w0 = p[2 * i] * scale_of(cur.vs[q], 2 * i), w1 = p[2 * i + 1] * scale_of(cur.vs[q], 2 * i + 1);
+                    if (!full) {                        // a masked token's scale may be anything
+                        w0 = (vis >> (2 * i)) & 1 ? w0 : 0.f;
+                        w1 = (vis >> (2 * i + 1)) & 1 ? w1 : 0.f;
+                    }
+                    wv[i] = bf16_pair(w0, w1);
+                }
+                const bf16x8 wf = __builtin_bit_cast(bf16x8, make_uint4(wv[0], wv[1], wv[2], wv[3]));
+                corr[q] = mfma16(ones, wf, corr[q]);
+#pragma unroll
+                for (int i = q * (NV / NG); i < (q + 1) * (NV / NG); ++i)
+                    acc[i] = mfma16(unit_bf16<BITS>(&cur.v[i * KU]), wf, acc[i]);
+            }
+        }
+        cur = nxt;
+        page = pnext;
+    }
+
+    // ---- join the waves
+    lrun += __shfl_xor(lrun, 16);
+    lrun += __shfl_xor(lrun, 32);
+    if (g == 0) {
+        sml[0][wave][m] = mrun;
+        sml[1][wave][m] = lrun;
+    }
+    __syncthreads();
+    {
+        float mx = sml[0][0][m];
+#pragma unroll
+        for (int x = 1; x < kWaves; ++x) mx = fmaxf(mx, sml[0][x][m]);
+        const float f = mrun == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(mrun - mx);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const float o = acc[i][x] - code_offset<BITS>() * corr[i / (NV / NG)][x];
+                sm[(wave * kCols + m) * (D + 4) + value_feature<BITS>(i, 4 * g + x)] = mrun == neg_inf() ? 0.f : o * f;
+            }
+    }
+    __syncthreads();
+    const int r = tid / (D / 8), j = tid % (D / 8), cr = ct * kCols + r;
+    if (D == 64 && r >= kCols) return;
+    float mx = sml[0][0][r], l = 0.f;
+#pragma unroll
+    for (int x = 1; x < kWaves; ++x) mx = fmaxf(mx, sml[0][x][r]);
+    float o[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = 0.f;
+#pragma unroll
+    for (int x = 0; x < kWaves; ++x) {
+        if (sml[0][x][r] != neg_inf()) l += sml[1][x][r] * __builtin_amdgcn_exp2f(sml[0][x][r] - mx);
+        const float4 *p = reinterpret_cast<const float4 *>(sm + (x * kCols + r) * (D + 4) + 8 * j);
+        const float4 u = p[0], v = p[1];
+        o[0] += u.x; o[1] += u.y; o[2] += u.z; o[3] += u.w;
+        o[4] += v.x; o[5] += v.y; o[6] += v.z; o[7] += v.w;
+    }
+    const int64_t row = s0 + cr / a.G;
+    const int head = h * a.G + cr % a.G;
+    if (a.splits == 1) {
+        finish_row<D, ROT>(a, row, head, j, o, mx, l, cr < ncol);
+    } else if (cr < ncol) {
+        const int64_t rows = (int64_t)a.total * a.hq, at = split * rows + row * a.hq + head;
+        if (j == 0) {
+            a.ws_ml[2 * at] = mx;
+            a.ws_ml[2 * at + 1] = l;
+        }
+        if (mx != neg_inf()) {
+            float4 *p = reinterpret_cast<float4 *>(a.ws_part + at * D + 8 * j);
+            p[0] = make_float4(o[0], o[1], o[2], o[3]);
+            p[1] = make_float4(o[4], o[5], o[6], o[7]);
+        }
+    }
+}
+
+// One workgroup of 256 threads per (query row, head): 2048 / D groups of D / 8
+// lanes take the splits in turn and are joined through LDS.
+template <int D, bool ROT>
+__global__ __launch_bounds__(256) void k_cache_attn_join(CacheAttnArgs a) {
+    constexpr int NGRP = 2048 / D;
+    const int head = blockIdx.x % a.hq, row = blockIdx.x / a.hq;
+    // rows that no sequence of the call has are left as they are
+    __shared__ int owned;
+    __shared__ float so[NGRP][D], sl[NGRP], sm[NGRP];
+    const int tid = threadIdx.x, grp = tid / (D / 8), j = tid % (D / 8);
+    if (tid == 0) owned = 0;
+    __syncthreads();
+    for (int b = tid; b < a.c.batch; b += 256) {
+        int s0;
+        const int n = min(ragged_rows(a.starts, b, a.total, &s0), a.max_q);
+        if (row >= s0 && row < s0 + n) owned = 1;
+    }
+    __syncthreads();
+    if (!owned) return;
+    const int64_t rows = (int64_t)a.total * a.hq, at = (int64_t)row * a.hq + head;
+    float m = neg_inf(), l = 0.f, o[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = 0.f;
+    for (int s = grp; s < a.splits; s += NGRP) {
+        const float ms = a.ws_ml[2 * (s * rows + at)], ls = a.ws_ml[2 * (s * rows + at) + 1];
+        if (ms == neg_inf()) continue;
+        const float mn = fmaxf(m, ms);
+        const float f0 = m == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(m - mn), f1 = __builtin_amdgcn_exp2f(ms - mn);
+        const float4 *p = reinterpret_cast<const float4 *>(a.ws_part + (s * rows + at) * D + 8 * j);
+        const float4 x = p[0], y = p[1];
+        const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = fmaf(o[e], f0, v[e] * f1);
+        l = fmaf(l, f0, ls * f1);
+        m = mn;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) so[grp][8 * j + e] = o[e];
+    if (j == 0) {
+        sm[grp] = m;
+        sl[grp] = l;
+    }
+    __syncthreads();
+    if (tid >= 64) return;                              // one wave (whole, for the lane exchanges) finishes the row
+    const int jj = tid % (D / 8);
+    float mt = neg_inf(), lt = 0.f, ot[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ot[e] = 0.f;
+    for (int x = 0; x < NGRP; ++x) mt = fmaxf(mt, sm[x]);
+    for (int x = 0; x < NGRP; ++x) {
+        if (sm[x] == neg_inf()) continue;
+        const float f = __builtin_amdgcn_exp2f(sm[x] - mt);
+        lt = fmaf(sl[x], f, lt);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ot[e] = fmaf(so[x][8 * jj + e], f, ot[e]);
+    }
+    finish_row<D, ROT>(a, row, head, jj, ot, mt, lt, tid < D / 8);
+}
+
+// ---------------------------------------------------------------- launchers
+template <int D, int BITS, bool ROT>
+static hipError_t attn_launch(const CacheAttnArgs &a, hipStream_t s) {
+    const int ctiles = (int)(((int64_t)a.max_q * a.G + kCols - 1) / kCols);
+    const int64_t grid = (int64_t)a.splits * ctiles * a.c.H * a.c.batch, rows = (int64_t)a.total * a.hq;
+    if (grid > 0x7FFFFFFF || rows > 0x7FFFFFFF) return hipErrorInvalidValue;
+    {
+        KTimeScope kts("k_cache_attn", s);
+        hipLaunchKernelGGL((k_cache_attn<D, BITS, ROT>), dim3((unsigned)grid), dim3(64 * kWaves), 0, s, a, ctiles);
+        if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    }
+    if (a.splits > 1) {
+        KTimeScope kts("k_cache_attn_join", s);
+        hipLaunchKernelGGL((k_cache_attn_join<D, ROT>), dim3((unsigned)rows), dim3(256), 0, s, a);
+    }
+    return hipGetLastError();
+}
+template <int D>
+static hipError_t attn_d(const CacheAttnArgs &a, int bits, bool rotate, hipStream_t s) {
+    if (bits == 4) return rotate ? attn_launch<D, 4, true>(a, s) : attn_launch<D, 4, false>(a, s);
+    return rotate ? attn_launch<D, 8, true>(a, s) : attn_launch<D, 8, false>(a, s);
+}
+hipError_t launch_cache_attention(const CacheAttnArgs &a, int d, int bits, bool rotate, hipStream_t s) {
+    return d == 128 ? attn_d<128>(a, bits, rotate, s) : attn_d<64>(a, bits, rotate, s);
+}
+
+}  // namespace jolt
