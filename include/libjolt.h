@@ -376,10 +376,11 @@ typedef struct {
  * (rows beyond it are left out).  max_len: the longest sequence as far as the
  * host knows; it sets how far the work is split, not what is read.
  *   out  bf16 rows;  lse  device fp32 [total][q_heads], NULL = not wanted
- * Rows past starts[batch] of out and lse are left as they are.  K codes enter
- * the products exactly; rotated queries are held as two bf16 parts (2^-17);
- * weights times value scales are rounded to bf16; sums and softmax statistics
- * are fp32.  The workspace (jolt_cache_attention_workspace_size() bytes for the
+ * Rows past starts[batch] of out and lse are left as they are.  K enters the
+ * products exactly; rotated queries are held in two parts (2^-16 or better);
+ * weights, with their value scales, are rounded to bf16 (few query rows) or
+ * fp16 (many); sums and softmax statistics are fp32.  A visible token stored as
+ * NaN makes the row's output NaN (its lse may be, too).  The workspace (jolt_cache_attention_workspace_size() bytes for the
  * same sizes, 16-byte aligned) carries split rows from launch to launch: calls
  * that may overlap (other streams, or replays of captured graphs) need one
  * each. */
@@ -475,7 +476,7 @@ size_t jolt_eigh_workspace_size(int32_t n, int32_t count, int32_t force_jacobi);
  * "k_eig_backtr", "k_eig_polish", "k_chol_inv",
  * "k_apply_linv", "k_gemm", "k_gram_rows", "k_reduce", "k_build_wt",
  * "k_jacobi_lds", "k_cache_append", "k_cache_read", "k_cache_keep",
- * "k_cache_attn", "k_cache_attn_join").  While a kernel's timer is on, each of its launches is
+ * "k_cache_attn", "k_cache_attn_wide", "k_cache_attn_join").  While a kernel's timer is on, each of its launches is
  * bracketed by a HIP event pair on its launch stream.  enable != 0 turns the
  * timer on and resets it; enable == 0 turns it off (the totals are kept).
  * Process-wide; h is used for error reporting only. */

@@ -18,8 +18,10 @@ LIB = os.path.join(HERE, "libjolt.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["api.cpp", "plan.cpp", "planner.cpp", "payload.cpp", "ktimer.cpp", "k_codec.hip", "k_plan.hip", "k_eig.hip", "k_orth.hip", "k_gemm.hip",
-           "k_attn.hip", "cache_api.cpp", "cache_args.cpp", "k_cache.hip", "k_cache_attn.hip"]
-HEADERS = ["bf16_split.h", "dev_common.h", "jolt_internal.h", "plan_kernels.h", "planner.h", "payload.h", "api_internal.h", "attn.h", "cache.h", "cache_dev.h"]
+           "k_attn.hip", "cache_api.cpp", "cache_args.cpp", "k_cache.hip",
+           "k_cache_attn.hip", "k_cache_attn_wide.hip"]
+HEADERS = ["bf16_split.h", "dev_common.h", "jolt_internal.h", "plan_kernels.h", "planner.h", "payload.h", "api_internal.h", "attn.h", "cache.h", "cache_dev.h",
+           "cache_attn_dev.h"]
 
 FLAGS = [
     "-O3", "-std=c++17", "-fPIC", "--offload-arch=gfx950",

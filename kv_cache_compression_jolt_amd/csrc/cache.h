@@ -66,6 +66,7 @@ JOLT_HD int cache_len(const CacheView &c, int b) {
 jolt_status cache_check(const jolt_cache *c, int32_t batch, const char **msg);
 jolt_status rows_check(const jolt_rows *r, int64_t total, int heads, int d, int elem, bool output, const char **msg);
 struct AttnPlan {
+    bool wide;                                       // many query columns: k_cache_attn_wide
     int splits;                                      // token ranges a row's cache is cut into
     size_t ml_off, part_off, bytes;                  // workspace: [splits][rows][2], [splits][rows][d] fp32
 };
@@ -110,7 +111,8 @@ struct CacheAttnArgs {
     float scale, cap;
     int window, total, max_q, hq, G, splits;
 };
-hipError_t launch_cache_attention(const CacheAttnArgs &a, int d, int bits, bool rotate, hipStream_t s);
+hipError_t launch_cache_attention(const CacheAttnArgs &a, bool wide, int d, int bits, bool rotate, hipStream_t s);
+hipError_t launch_cache_attn_wide(const CacheAttnArgs &a, int d, int bits, bool rotate, hipStream_t s);
 #endif
 
 }  // namespace jolt

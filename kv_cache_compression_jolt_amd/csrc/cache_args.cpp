@@ -73,14 +73,17 @@ jolt_status cache_attn_check(const jolt_cache *c, int32_t batch, int32_t total, 
     return JOLT_OK;
 }
 
-// Token ranges: enough workgroups for the 256 CUs (about four each), none of
-// fewer than 256 tokens.
+// Query columns of a KV head and sequence: up to 32 go to the narrow kernel
+// (tiles of 16), more to the wide one (tiles of 128).  Token ranges: enough
+// workgroups for the 256 CUs (about four narrow or two wide ones each), none of
+// fewer than 256 (512) tokens.
 AttnPlan cache_attn_plan(const jolt_cache &c, int batch, int64_t total, int max_q, int max_len, int q_heads) {
     AttnPlan p{};
-    const int64_t G = q_heads / c.H;
-    const int64_t tiles = std::max<int64_t>(1, (int64_t)batch * c.H * (((int64_t)max_q * G + 15) / 16));
-    const int64_t by_len = std::max<int64_t>(1, max_len / 256);
-    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(by_len, 1024 / tiles));
+    const int64_t cols = (int64_t)max_q * (q_heads / c.H);
+    p.wide = cols > 32;
+    const int64_t per = p.wide ? 128 : 16, want = p.wide ? 512 : 1024, least = p.wide ? 512 : 256;
+    const int64_t tiles = std::max<int64_t>(1, (int64_t)batch * c.H * ((cols + per - 1) / per));
+    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(max_len / least, want / tiles));
     if (p.splits > 1) {
         const size_t rows = (size_t)total * q_heads;
         p.ml_off = 0;

@@ -1,0 +1,120 @@
+// Device code shared by the token cache's attention kernels: which tokens a
+// query column sees, and the last steps of a row.
+#pragma once
+#include "cache_dev.h"
+
+namespace jolt {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
+
+// What a query column may see, in tokens: t >= first, and (t < prefix or
+// low <= t < hi); of a tree's slots those of its mask within the window.
+struct Column {
+    int pos, low, first, hi;
+    float slope;                          // slope * log2 e
+    uint64_t mask;
+
+    // column c of KV head h in sequence b (valid: c < n G), whose rows start at s0
+    __device__ __forceinline__ Column(const CacheAttnArgs &a, int s0, int base, int h, int c, bool valid) {
+        const int i = valid ? c / a.G : 0;
+        mask = 0;
+        pos = base + i;
+        if (a.tree) {
+            mask = valid ? a.tree[s0 + i] : 0;
+            pos = base + max(__popcll(mask) - 1, 0);
+        }
+        first = valid && a.first ? a.first[s0 + i] : 0;
+        low = a.window > 0 ? pos - a.window + 1 : -0x7FFFFFFF;
+        hi = a.tree ? base : pos + 1;
+        slope = a.slopes ? a.slopes[h * a.G + (valid ? c % a.G : 0)] * kLog2e : 0.f;
+    }
+    // whether token t is visible; *tp: its position
+    __device__ __forceinline__ bool sees(const CacheAttnArgs &a, int t, int s0, int n, int base, int len, int prefix,
+                                         int *tp) const {
+        *tp = t;
+        if (a.tree && t >= base) {
+            const int slot = t - base;
+            const bool in = slot < n && slot < kMaxKeep && t < len;
+            *tp = base + (in ? max(__popcll(a.tree[s0 + slot]) - 1, 0) : 0);
+            return in && ((mask >> (slot & 63)) & 1) && *tp >= low;
+        }
+        return t < len && t >= first && (t < prefix || (t >= low && t < hi));
+    }
+};
+
+// Token ranges of a set of columns: [lo_any, hi_any) holds every token some
+// column may see, apart from the prefix; every column sees all of [lo_all, hi_all).
+struct Reach {
+    int lo_any, hi_any, lo_all, hi_all, first_any;
+    __device__ __forceinline__ Reach(const Column &c, bool valid) {
+        const int lo = max(c.low, c.first);
+        lo_any = valid ? lo : 0x7FFFFFFF;
+        hi_any = valid ? c.hi : 0;
+        lo_all = valid ? lo : -0x7FFFFFFF;
+        hi_all = valid ? c.hi : 0x7FFFFFFF;
+        first_any = valid ? c.first : 0x7FFFFFFF;
+    }
+    // over aligned groups of W lanes
+    template <int W>
+    __device__ __forceinline__ void join() {
+#pragma unroll
+        for (int x = 1; x < W; x *= 2) {
+            lo_any = min(lo_any, __shfl_xor(lo_any, x));
+            hi_any = max(hi_any, __shfl_xor(hi_any, x));
+            lo_all = max(lo_all, __shfl_xor(lo_all, x));
+            hi_all = min(hi_all, __shfl_xor(hi_all, x));
+            first_any = min(first_any, __shfl_xor(first_any, x));
+        }
+    }
+    __device__ __forceinline__ void clip(const CacheAttnArgs &a, int len, int prefix) {
+        if (a.tree) hi_any = len;
+        hi_any = min(max(hi_any, prefix), len);
+        hi_all = min(hi_all, len);
+    }
+    // the first token any column may see, the prefix included
+    __device__ __forceinline__ int begin(int prefix) const {
+        return max(prefix > first_any ? min(first_any, lo_any) : lo_any, 0);
+    }
+};
+
+// out row: o (8 features of lane j of D/8), l and m (log2 domain) of the whole row
+template <int D, bool ROT>
+__device__ __forceinline__ void finish_row(const CacheAttnArgs &a, int64_t row, int head, int j, float (&o)[8], float m,
+                                           float l, bool store) {
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] *= inv;
+    if constexpr (ROT) {
+        fwht_row<D>(o, j);
+        const uint32_t sb = sign_byte(a.c.sv, j);
+        const float isd = D == 128 ? 0.08838834764831845f : 0.125f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = flip(o[e] * isd, (sb >> e) & 1);
+    }
+    if (!store) return;
+    float lse = l == 0.f ? neg_inf() : (m + __builtin_amdgcn_logf(l)) * kLn2;
+    const int64_t at = row * a.hq + head;
+    if (a.merge_out) {
+        const float l2 = a.merge_lse[at], mx = fmaxf(lse, l2);
+        const float w1 = mx == neg_inf() ? 0.f : __builtin_amdgcn_exp2f((lse - mx) * kLog2e);
+        const float w2 = mx == neg_inf() ? 0.f : __builtin_amdgcn_exp2f((l2 - mx) * kLog2e);
+        const float s = w1 + w2, is = s == 0.f ? 0.f : 1.f / s;
+        const float4 *p = reinterpret_cast<const float4 *>(a.merge_out + at * D + 8 * j);
+        const float4 x = p[0], y = p[1];
+        const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {                   // a part that saw nothing adds nothing, whatever its rows hold
+            const float p1 = w1 == 0.f ? 0.f : o[e] * w1, p2 = w2 == 0.f ? 0.f : v[e] * w2;
+            o[e] = (p1 + p2) * is;
+        }
+        lse = s == 0.f ? neg_inf() : mx + __builtin_amdgcn_logf(s) * kLn2;
+    }
+    uint16_t *dst = static_cast<uint16_t *>(a.out.ptr) + row * a.out.ts + head * a.out.hs + 8 * j;
+    *reinterpret_cast<uint4 *>(dst) =
+        make_uint4(bf16_pair(o[0], o[1]), bf16_pair(o[2], o[3]), bf16_pair(o[4], o[5]), bf16_pair(o[6], o[7]));
+    if (a.lse && j == 0) a.lse[at] = lse;
+}
+
+}  // namespace jolt

@@ -20,7 +20,7 @@
 #include <algorithm>
 
 #include "cache.h"
-#include "cache_dev.h"
+#include "cache_attn_dev.h"
 #include "jolt_internal.h"
 #include "ktimer.h"
 
@@ -28,11 +28,8 @@ namespace jolt {
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kCols = 16;                 // query columns of a tile
 constexpr int kWaves = 4;
-
-__device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 
 __device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
@@ -112,51 +109,6 @@ template <int BITS>
 __device__ __forceinline__ constexpr int value_feature(int i, int m) {
     constexpr int per = 16 / BITS;                      // units (features) of a 16-byte load
     return (i / per) * (16 * per) + m * per + i % per;
-}
-
-// Query column state: what a row may see, in tokens
-struct Column {
-    int pos, low, first, hi;              // t >= first, and (t < prefix or low <= t < hi)
-    float slope;                          // slope * log2 e
-    uint64_t mask;                        // tree: visible slots
-};
-
-// out row: o (8 features of lane j of D/8), l and m (log2 domain) of the whole row
-template <int D, bool ROT>
-__device__ __forceinline__ void finish_row(const CacheAttnArgs &a, int64_t row, int head, int j, float (&o)[8], float m,
-                                           float l, bool store) {
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] *= inv;
-    if constexpr (ROT) {
-        fwht_row<D>(o, j);
-        const uint32_t sb = sign_byte(a.c.sv, j);
-        const float isd = D == 128 ? 0.08838834764831845f : 0.125f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = flip(o[e] * isd, (sb >> e) & 1);
-    }
-    if (!store) return;
-    float lse = l == 0.f ? neg_inf() : (m + __builtin_amdgcn_logf(l)) * kLn2;
-    const int64_t at = row * a.hq + head;
-    if (a.merge_out) {
-        const float l2 = a.merge_lse[at], mx = fmaxf(lse, l2);
-        const float w1 = mx == neg_inf() ? 0.f : __builtin_amdgcn_exp2f((lse - mx) * kLog2e);
-        const float w2 = mx == neg_inf() ? 0.f : __builtin_amdgcn_exp2f((l2 - mx) * kLog2e);
-        const float s = w1 + w2, is = s == 0.f ? 0.f : 1.f / s;
-        const float4 *p = reinterpret_cast<const float4 *>(a.merge_out + at * D + 8 * j);
-        const float4 x = p[0], y = p[1];
-        const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {                   // a part that saw nothing adds nothing, whatever its rows hold
-            const float p1 = w1 == 0.f ? 0.f : o[e] * w1, p2 = w2 == 0.f ? 0.f : v[e] * w2;
-            o[e] = (p1 + p2) * is;
-        }
-        lse = s == 0.f ? neg_inf() : mx + __builtin_amdgcn_logf(s) * kLn2;
-    }
-    uint16_t *dst = static_cast<uint16_t *>(a.out.ptr) + row * a.out.ts + head * a.out.hs + 8 * j;
-    *reinterpret_cast<uint4 *>(dst) =
-        make_uint4(bf16_pair(o[0], o[1]), bf16_pair(o[2], o[3]), bf16_pair(o[4], o[5]), bf16_pair(o[6], o[7]));
-    if (a.lse && j == 0) a.lse[at] = lse;
 }
 
 }  // namespace
@@ -255,37 +207,12 @@ __global__ __launch_bounds__(64 * kWaves) void k_cache_attn(CacheAttnArgs a, int
     // ---- what the columns see
     const int c = ct * kCols + m, ncol = n * a.G;
     const bool cv = c < ncol;
-    Column col;
-    {
-        const int i = cv ? c / a.G : 0;
-        col.mask = 0;
-        col.pos = base + i;
-        if (a.tree) {
-            col.mask = cv ? a.tree[s0 + i] : 0;
-            col.pos = base + max(__popcll(col.mask) - 1, 0);
-        }
-        col.first = cv && a.first ? a.first[s0 + i] : 0;
-        col.low = a.window > 0 ? col.pos - a.window + 1 : -0x7FFFFFFF;
-        col.hi = a.tree ? base : col.pos + 1;
-        col.slope = a.slopes ? a.slopes[h * a.G + (cv ? c % a.G : 0)] * kLog2e : 0.f;
-    }
-    // tokens any column may see [lo_any, hi_any) apart from the prefix, and those
-    // all columns see [lo_all, hi_all)
-    int lo_any = cv ? max(col.low, col.first) : 0x7FFFFFFF, hi_any = cv ? col.hi : 0;
-    int lo_all = cv ? max(col.low, col.first) : -0x7FFFFFFF, hi_all = cv ? col.hi : 0x7FFFFFFF;
-    int first_any = cv ? col.first : 0x7FFFFFFF;
-#pragma unroll
-    for (int x = 1; x < 16; x *= 2) {
-        lo_any = min(lo_any, __shfl_xor(lo_any, x));
-        hi_any = max(hi_any, __shfl_xor(hi_any, x));
-        lo_all = max(lo_all, __shfl_xor(lo_all, x));
-        hi_all = min(hi_all, __shfl_xor(hi_all, x));
-        first_any = min(first_any, __shfl_xor(first_any, x));
-    }
-    if (a.tree) hi_any = len;
-    hi_any = min(max(hi_any, prefix), len);
-    hi_all = min(hi_all, len);
-    const int begin = max(prefix > first_any ? min(first_any, lo_any) : lo_any, 0);
+    const Column col(a, s0, base, h, c, cv);
+    Reach reach(col, cv);
+    reach.join<16>();
+    reach.clip(a, len, prefix);
+    const int lo_any = reach.lo_any, hi_any = reach.hi_any, lo_all = reach.lo_all, hi_all = reach.hi_all;
+    const int begin = reach.begin(prefix);
 
     // ---- this workgroup's blocks, this wave's every kWaves-th
     const int blk0 = begin >> 5, nblk = hi_any > begin ? ((hi_any + 31) >> 5) - blk0 : 0;
@@ -354,17 +281,8 @@ __global__ __launch_bounds__(64 * kWaves) void k_cache_attn(CacheAttnArgs a, int
                 vis = 0;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const int t = t0 + 8 * g + e;
-                    int tp = t;
-                    bool v;
-                    if (a.tree && t >= base) {
-                        const int slot = t - base;
-                        const bool in = slot < n && slot < kMaxKeep && t < len;
-                        tp = base + (in ? max(__popcll(a.tree[s0 + slot]) - 1, 0) : 0);
-                        v = in && ((col.mask >> (slot & 63)) & 1) && tp >= col.low;
-                    } else {
-                        v = t < len && t >= col.first && (t < prefix || (t >= col.low && t < col.hi));
-                    }
+                    int tp;
+                    const bool v = col.sees(a, t0 + 8 * g + e, s0, n, base, len, prefix, &tp);
                     vis |= (uint32_t)v << e;
                     s[e] -= col.slope * fabsf((float)(col.pos - tp));
                     s[e] = v ? s[e] : neg_inf();
@@ -534,26 +452,28 @@ __global__ __launch_bounds__(256) void k_cache_attn_join(CacheAttnArgs a) {
 template <int D, int BITS, bool ROT>
 static hipError_t attn_launch(const CacheAttnArgs &a, hipStream_t s) {
     const int ctiles = (int)(((int64_t)a.max_q * a.G + kCols - 1) / kCols);
-    const int64_t grid = (int64_t)a.splits * ctiles * a.c.H * a.c.batch, rows = (int64_t)a.total * a.hq;
-    if (grid > 0x7FFFFFFF || rows > 0x7FFFFFFF) return hipErrorInvalidValue;
-    {
-        KTimeScope kts("k_cache_attn", s);
-        hipLaunchKernelGGL((k_cache_attn<D, BITS, ROT>), dim3((unsigned)grid), dim3(64 * kWaves), 0, s, a, ctiles);
-        if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    }
-    if (a.splits > 1) {
-        KTimeScope kts("k_cache_attn_join", s);
-        hipLaunchKernelGGL((k_cache_attn_join<D, ROT>), dim3((unsigned)rows), dim3(256), 0, s, a);
-    }
+    const int64_t grid = (int64_t)a.splits * ctiles * a.c.H * a.c.batch;
+    if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+    KTimeScope kts("k_cache_attn", s);
+    hipLaunchKernelGGL((k_cache_attn<D, BITS, ROT>), dim3((unsigned)grid), dim3(64 * kWaves), 0, s, a, ctiles);
     return hipGetLastError();
 }
 template <int D>
-static hipError_t attn_d(const CacheAttnArgs &a, int bits, bool rotate, hipStream_t s) {
-    if (bits == 4) return rotate ? attn_launch<D, 4, true>(a, s) : attn_launch<D, 4, false>(a, s);
-    return rotate ? attn_launch<D, 8, true>(a, s) : attn_launch<D, 8, false>(a, s);
+static hipError_t attn_d(const CacheAttnArgs &a, bool wide, int bits, bool rotate, hipStream_t s) {
+    hipError_t e;
+    if (wide) e = launch_cache_attn_wide(a, D, bits, rotate, s);
+    else if (bits == 4) e = rotate ? attn_launch<D, 4, true>(a, s) : attn_launch<D, 4, false>(a, s);
+    else e = rotate ? attn_launch<D, 8, true>(a, s) : attn_launch<D, 8, false>(a, s);
+    if (e != hipSuccess || a.splits == 1) return e;
+    const int64_t rows = (int64_t)a.total * a.hq;
+    if (rows > 0x7FFFFFFF) return hipErrorInvalidValue;
+    KTimeScope kts("k_cache_attn_join", s);
+    if (rotate) hipLaunchKernelGGL((k_cache_attn_join<D, true>), dim3((unsigned)rows), dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((k_cache_attn_join<D, false>), dim3((unsigned)rows), dim3(256), 0, s, a);
+    return hipGetLastError();
 }
-hipError_t launch_cache_attention(const CacheAttnArgs &a, int d, int bits, bool rotate, hipStream_t s) {
-    return d == 128 ? attn_d<128>(a, bits, rotate, s) : attn_d<64>(a, bits, rotate, s);
+hipError_t launch_cache_attention(const CacheAttnArgs &a, bool wide, int d, int bits, bool rotate, hipStream_t s) {
+    return d == 128 ? attn_d<128>(a, wide, bits, rotate, s) : attn_d<64>(a, wide, bits, rotate, s);
 }
 
 }  // namespace jolt

@@ -1,0 +1,550 @@
+// Attention over the token cache for many query rows (prompt chunks, trees):
+// the same sums as k_cache_attn.hip, with 64-token tiles of the cache staged
+// once per workgroup in LDS and shared by its waves of 32 query columns.
+//
+// Staging undoes the quantization, so that a score costs one product and no
+// scaling: rows go to LDS in fp16 as q sc 2^-E, with E the tile's largest scale
+// exponent.  For 4-bit codes that is exact (3 + 8 significant bits); for 8-bit
+// ones K holds the codes alone (their scales multiply the scores of each group
+// of 64 in fp32) and V is rounded to fp16 (2^-11).  A scale more than 2^26
+// (4 bits; 8 bits: 2^22) below the tile's largest counts as nothing.  Queries
+// are divided by a power of two that brings their largest feature to [1, 2) and
+// held in fp16: exact for bf16 queries, two parts (2^-22) for rotated ones.
+// Weights are rounded to fp16 (2^-11).
+//
+// Products are S^T = K Q^T and O^T = V^T P^T in 32x32x16, and as in the narrow
+// kernel a lane's scores are, in order, its operand of the second product.
+#include <algorithm>
+
+#include "cache.h"
+#include "cache_attn_dev.h"
+#include "jolt_internal.h"
+#include "ktimer.h"
+
+namespace jolt {
+
+namespace {
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef short s16x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kTile = 64;                              // tokens of a tile
+
+__device__ __forceinline__ f32x16 mfma32(f16x8 a, f16x8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ uint32_t f16_pair(float a, float b) {
+    const f32x2 v = {a, b};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
+}
+__device__ __forceinline__ f16x2 h2(uint32_t w) { return __builtin_bit_cast(f16x2, w); }
+__device__ __forceinline__ uint32_t u32(f16x2 v) { return __builtin_bit_cast(uint32_t, v); }
+
+// a unit of 8 codes as signed fp16 integers, exact.  4 bits: a nibble under the
+// exponent of 1024 is 1024 + u, or 1024 + 16 u from the next nibble up.
+template <int BITS>
+__device__ __forceinline__ void unit_f16(const uint32_t *w, f16x2 (&x)[4]) {
+    if constexpr (BITS == 4) {
+        const f16x2 c0 = {(_Float16)-1032.f, (_Float16)-1032.f}, c1 = {(_Float16)-72.f, (_Float16)-72.f};
+        const f16x2 r = {(_Float16)0.0625f, (_Float16)0.0625f};
+        const uint32_t a = w[0], b = a >> 8;
+        x[0] = h2((a & 0x000F000Fu) | 0x64006400u) + c0;
+        x[1] = __builtin_elementwise_fma(h2((a & 0x00F000F0u) | 0x64006400u), r, c1);
+        x[2] = h2((b & 0x000F000Fu) | 0x64006400u) + c0;
+        x[3] = __builtin_elementwise_fma(h2((b & 0x00F000F0u) | 0x64006400u), r, c1);
+    } else {
+        const f16x2 c0 = {(_Float16)-1152.f, (_Float16)-1152.f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)                    // bytes 2 i, 2 i + 1 under the exponent of 1024
+            x[i] = h2(__builtin_amdgcn_perm(w[i >> 1], 0x64646464u, (i & 1) ? 0x00070006u : 0x00050004u)) + c0;
+    }
+}
+
+// bf16 scales (two) as fp16 with field exponent e + shift; below the range: 0
+__device__ __forceinline__ f16x2 scale_f16(uint32_t two, int shift) {
+    s16x2 v = __builtin_bit_cast(s16x2, two);
+    const short d = (short)(shift << 7);
+    v += s16x2{d, d};
+    v = __builtin_elementwise_max(v, s16x2{0, 0});
+    v <<= s16x2{3, 3};
+    return __builtin_bit_cast(f16x2, v);
+}
+
+__device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
+    v = group_umax<16>(v);
+    const int i = (int)v;
+    const uint32_t a = max((uint32_t)__builtin_amdgcn_readlane(i, 0), (uint32_t)__builtin_amdgcn_readlane(i, 16));
+    const uint32_t b = max((uint32_t)__builtin_amdgcn_readlane(i, 32), (uint32_t)__builtin_amdgcn_readlane(i, 48));
+    return max(a, b);
+}
+
+// largest finite exponent field of two packed bf16 scales (sign clear)
+__device__ __forceinline__ uint32_t max_exponent(uint32_t two) {
+    const uint32_t a = (two >> 7) & 0xFFu, b = (two >> 23) & 0xFFu;
+    return max(a == 255u ? 0u : a, b == 255u ? 0u : b);
+}
+
+// One thread's share of a tile: UPT units of K and of V, the scales they need,
+// and the tile's scales for their largest exponent (two tokens of a group to a
+// lane: lanes 0..31 group 0, 32..63 group 1).
+template <int D, int BITS, int NT>
+struct TileRegs {
+    static constexpr int kU = BITS / 4;                // dwords of a unit
+    static constexpr int UPT = kTile * D / 8 / NT;
+    static constexpr int FS = NT / 8;                  // a thread's V features: f, f + FS, ...
+    uint32_t k[UPT * kU], v[UPT * kU], vs[D / 64][4];
+    uint32_t allk, allv;
+    uint16_t ks[D / 64], vbad;
+};
+
+}  // namespace
+
+template <int D, int BITS, bool ROT, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a, int ctiles) {
+    constexpr int NT = 64 * NW, NK = D / 16, NF = D / 32, NG = D / 64, NP = ROT ? 2 : 1;
+    constexpr bool kPost = BITS == 8;                  // K scales multiply the scores
+    constexpr int kTop = BITS == 4 ? 27 : 23;          // fp16 exponent field of the largest scale
+    constexpr int kKStride = kTile * 16 + 32;          // bytes of a K chunk (8 features of 64 tokens), padded
+    constexpr int kKBytes = D / 8 * kKStride, kVBytes = kTile / 8 * D * 16;
+    constexpr int kSBytes = kPost ? NG * kTile * 4 : 0;
+    constexpr int kBuf = kKBytes + kVBytes + kSBytes;
+    constexpr int kOutCols = 16;                       // columns of a wave that leave through LDS together
+    constexpr int kOut = NW * kOutCols * (D + 4) * 4;
+    __shared__ __align__(16) uint8_t lds[2 * kBuf > kOut ? 2 * kBuf : kOut];
+    __shared__ int reach_all[NW][3];
+    typedef TileRegs<D, BITS, NT> Regs;
+    constexpr int UPT = Regs::UPT, KU = Regs::kU, FS = Regs::FS;
+
+    // contiguous ranges of (sequence, head, columns, split) to an XCD: tiles of one head share its L2
+    int64_t w = blockIdx.x;
+    if (gridDim.x % 8 == 0) w = (w % 8) * (gridDim.x / 8) + w / 8;
+    const int split = (int)(w % a.splits);
+    w /= a.splits;
+    const int ct = ctiles - 1 - (int)(w % ctiles);     // later rows see more: they start first
+    w /= ctiles;
+    const int h = (int)(w % a.c.H), b = (int)(w / a.c.H);
+    int s0;
+    const int nall = ragged_rows(a.starts, b, a.total, &s0), n = min(nall, a.max_q), ncol = n * a.G;
+    if (ct * 32 * NW >= ncol) return;
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, m = lane & 31, hh = lane >> 5;
+    const int len = cache_len(a.c, b), base = a.c.lens[b] - nall;
+    const int prefix = a.prefix ? a.prefix[b] : 0;
+    const int c0 = (ct * NW + wave) * 32;              // this wave's columns
+    const bool active = c0 < ncol;
+
+    // ---- queries: 16 columns of the wave at a time through its part of LDS
+    f16x8 qf[NP][NK];
+    float qmul = 0.f;                                  // what the column's scores are multiplied with
+    {
+        float *sq = reinterpret_cast<float *>(lds) + wave * kOutCols * (D + 4);
+        constexpr int RL = D / 8, RW = 64 / RL;        // lanes of a row, rows of a pass
+        const int r = lane / RL, j = lane % RL;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int it = 0; it < kOutCols / RW; ++it) {
+                const int cc = it * RW + r, c = c0 + half * 16 + cc;
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = 0.f;
+                if (c < ncol) {
+                    const int i = c / a.G, hd = h * a.G + c % a.G;
+                    const uint4 v = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q.ptr) +
+                                                                     (int64_t)(s0 + i) * a.q.ts + hd * a.q.hs + 8 * j);
+                    const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = __uint_as_float((e & 1) ? (q[e >> 1] & 0xFFFF0000u) : (q[e >> 1] << 16));
+                }
+                if constexpr (ROT) {
+                    const uint32_t sb = sign_byte(a.c.sk, j);
+                    const float isd = D == 128 ? 0.08838834764831845f : 0.125f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = flip(x[e], (sb >> e) & 1);
+                    fwht_row<D>(x, j);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] *= isd;
+                }
+                uint32_t am = 0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) am = max(am, __float_as_uint(x[e]) & 0x7FFFFFFFu);
+                am = group_umax<RL>(am);
+                // 2^-e brings the largest feature to [1, 2); its inverse goes into qmul
+                const int ex = min(max((int)(am >> 23), 1), 253);
+                const float down = __uint_as_float((uint32_t)(254 - ex) << 23), up = __uint_as_float((uint32_t)ex << 23);
+                float4 *p = reinterpret_cast<float4 *>(sq + cc * (D + 4) + 8 * j);
+                p[0] = make_float4(x[0] * down, x[1] * down, x[2] * down, x[3] * down);
+                p[1] = make_float4(x[4] * down, x[5] * down, x[6] * down, x[7] * down);
+                if (j == 0) sq[cc * (D + 4) + D] = up;
+            }
+            wave_lds_sync();
+            if ((m >> 4) == half) {
+                const float *row = sq + (m & 15) * (D + 4);
+                qmul = row[D];
+#pragma unroll
+                for (int k = 0; k < NK; ++k) {
+                    const float *p = row + 16 * k + 8 * hh;
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float x0 = p[2 * i], x1 = p[2 * i + 1];
+                        hi[i] = f16_pair(x0, x1);
+                        lo[i] = f16_pair(x0 - (float)h2(hi[i])[0], x1 - (float)h2(hi[i])[1]);
+                    }
+                    qf[0][k] = __builtin_bit_cast(f16x8, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+                    if constexpr (ROT) qf[NP - 1][k] = __builtin_bit_cast(f16x8, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+                }
+            }
+            wave_lds_sync();
+        }
+    }
+
+    // ---- what the wave's columns see, and the workgroup's range of tiles
+    const int c = c0 + m;
+    const bool cv = c < ncol;
+    const Column col(a, s0, base, h, c, cv);
+    Reach reach(col, cv);
+    reach.join<32>();
+    reach.clip(a, len, prefix);
+    if (lane == 0) {
+        reach_all[wave][0] = active ? reach.begin(prefix) : 0x7FFFFFFF;
+        reach_all[wave][1] = active ? reach.hi_any : 0;
+        reach_all[wave][2] = active ? reach.lo_any : 0x7FFFFFFF;
+    }
+    __syncthreads();
+    int begin = 0x7FFFFFFF, end = 0, lo_any = 0x7FFFFFFF;
+#pragma unroll
+    for (int x = 0; x < NW; ++x) {
+        begin = min(begin, reach_all[x][0]);
+        end = max(end, reach_all[x][1]);
+        lo_any = min(lo_any, reach_all[x][2]);
+    }
+    const int tile0 = begin / kTile, ntile = end > begin ? (end + kTile - 1) / kTile - tile0 : 0;
+    const int per = (ntile + a.splits - 1) / a.splits;
+    const int ts = tile0 + split * per, te = min(ts + per, tile0 + ntile);
+
+    const int P = 1 << a.c.page_shift;
+    const PageLayout pl = page_layout(P, D, BITS);
+    f32x16 acc[NF];
+#pragma unroll
+    for (int i = 0; i < NF; ++i) acc[i] = f32x16{};
+    float mrun = neg_inf(), lrun = 0.f;
+    int erun = kTop;                                   // exponent field of acc's unit: the largest V scale so far
+    const float mul = a.scale * kLog2e * qmul, cap_in = a.cap > 0.f ? a.scale / a.cap * (2.f * kLog2e) * qmul : 0.f;
+
+    // tiles between a prefix and the window are skipped by the whole workgroup
+    auto next_tile = [&](int t) {
+        const int skip_to = lo_any / kTile;
+        return t * kTile >= prefix && t < skip_to ? skip_to : t;
+    };
+    auto page_of = [&](int t, int half) -> int {
+        return t < te ? cache_page(a.c, b, t * kTile + 32 * half) : -1;
+    };
+    // units of K: consecutive ones of a row; units of V: features f, f + FS, .. of a block of 8 tokens
+    const int kidx = tid * UPT, ktok = kidx / (D / 8), ku0 = kidx % (D / 8);
+    const int vblk = tid / FS, vf = tid % FS;
+    Regs rg;
+    auto fetch = [&](int t, int p0, int p1) {
+        const int t0 = t * kTile;
+        // tokens without a page read page 0 of the pool's first head (never used: their scales count as 0);
+        // a call with pages == 0 has no valid page and fetches nothing
+        const uint8_t *b0 = a.c.pool + (p0 >= 0 ? cache_block_offset(a.c, p0, h) : 0);
+        const uint8_t *b1 = a.c.pool + (p1 >= 0 ? cache_block_offset(a.c, p1, h) : 0);
+        const int i0 = t0 & (P - 1), i1 = (t0 + 32) & (P - 1);
+        {
+            const uint8_t *kb = ktok < 32 ? b0 : b1;
+            const int tin = ktok < 32 ? i0 + ktok : i1 + ktok - 32;
+            const uint8_t *p = kb + tin * (D * BITS / 8) + ku0 * (4 * KU);
+            constexpr int N = UPT * KU;
+            if constexpr (N == 1) rg.k[0] = *reinterpret_cast<const uint32_t *>(p);
+            else if constexpr (N == 2) {
+                const uint2 v = *reinterpret_cast<const uint2 *>(p);
+                rg.k[0] = v.x; rg.k[1] = v.y;
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; i += 4) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(p + 4 * i);
+                    rg.k[i] = v.x; rg.k[i + 1] = v.y; rg.k[i + 2] = v.z; rg.k[i + 3] = v.w;
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < NG; ++q) rg.ks[q] = reinterpret_cast<const uint16_t *>(kb + pl.k_scales)[q * P + tin];
+            rg.vbad = reinterpret_cast<const uint16_t *>(kb + pl.v_scales)[tin];
+        }
+        {
+            const uint8_t *vb = vblk < 4 ? b0 : b1;
+            const int tin = vblk < 4 ? i0 + 8 * vblk : i1 + 8 * vblk - 32;
+            const uint8_t *p = vb + pl.v_codes + (tin >> 3) * (D * BITS);
+#pragma unroll
+            for (int x = 0; x < UPT; ++x) {
+                if constexpr (KU == 1) rg.v[x] = reinterpret_cast<const uint32_t *>(p)[vf + FS * x];
+                else {
+                    const uint2 v = reinterpret_cast<const uint2 *>(p)[vf + FS * x];
+                    rg.v[2 * x] = v.x; rg.v[2 * x + 1] = v.y;
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < NG; ++q) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(vb + pl.v_scales + (q * P + tin) * 2);
+                rg.vs[q][0] = v.x; rg.vs[q][1] = v.y; rg.vs[q][2] = v.z; rg.vs[q][3] = v.w;
+            }
+        }
+        {
+            const int q = NG == 2 ? hh : 0;
+            const uint8_t *sb = m < 16 ? b0 : b1;
+            const int tin = m < 16 ? i0 + 2 * m : i1 + 2 * m - 32;
+            rg.allk = *reinterpret_cast<const uint32_t *>(sb + pl.k_scales + (q * P + tin) * 2);
+            rg.allv = *reinterpret_cast<const uint32_t *>(sb + pl.v_scales + (q * P + tin) * 2);
+        }
+    };
+    // registers -> LDS; returns the exponent field of the tile's K unit, and raises enext
+    int enext = kTop;                                  // (the floor keeps a zero scale zero)
+    auto stage = [&](int t, int p0, int p1, uint8_t *buf) -> int {
+        const int t0 = t * kTile;
+        const int lim0 = p0 >= 0 ? len : 0, lim1 = p1 >= 0 ? len : 0;      // tokens below these count, by half
+        // two tokens a lane: keep those that count
+        const int te0 = t0 + 2 * m, lim = m < 16 ? lim0 : lim1;
+        const uint32_t keep = (te0 < lim ? 0xFFFFu : 0u) | (te0 + 1 < lim ? 0xFFFF0000u : 0u);
+        const int ek = kPost ? 0 : max((int)wave_umax(max_exponent(rg.allk & keep)), kTop);
+        enext = max(enext, (int)wave_umax(max_exponent(rg.allv & keep)));
+        {
+            const bool on = t0 + ktok < (ktok < 32 ? lim0 : lim1);
+            const bool bad = (rg.vbad & 0x7F80u) == 0x7F80u || (rg.ks[0] & 0x7F80u) == 0x7F80u;
+#pragma unroll
+            for (int x = 0; x < UPT; ++x) {
+                const int u = ku0 + x, g = u / (D / 32), kk = u % (D / 32);
+                f16x2 y[4];
+                unit_f16<BITS>(&rg.k[x * KU], y);
+                if constexpr (!kPost) {
+                    const uint32_t s = on ? rg.ks[kk / 2] : 0u;
+                    f16x2 sc = scale_f16(s | (s << 16), kTop - ek);
+                    if (bad && on) sc = h2(0x7E007E00u);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) y[i] *= sc;
+                }
+                *reinterpret_cast<uint4 *>(buf + (4 * kk + g) * kKStride + ktok * 16) =
+                    make_uint4(u32(y[0]), u32(y[1]), u32(y[2]), u32(y[3]));
+            }
+            if constexpr (kPost) {
+                if (ku0 == 0)
+#pragma unroll
+                    for (int q = 0; q < NG; ++q)
+                        reinterpret_cast<float *>(buf + kKBytes + kVBytes)[q * kTile + ktok] =
+                            !on ? 0.f : (bad ? __builtin_nanf("") : bf16_to_f32(rg.ks[q]));
+            }
+        }
+        const int tv = t0 + 8 * vblk, vlim = vblk < 4 ? lim0 : lim1;
+        f16x2 sc[NG][4];
+#pragma unroll
+        for (int q = 0; q < NG; ++q)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t s = rg.vs[q][i];
+                if (tv + 2 * i >= vlim || (s & 0x7F80u) == 0x7F80u) s &= 0xFFFF0000u;
+                if (tv + 2 * i + 1 >= vlim || (s & 0x7F800000u) == 0x7F800000u) s &= 0x0000FFFFu;
+                sc[q][i] = scale_f16(s, kTop - enext);
+            }
+#pragma unroll
+        for (int x = 0; x < UPT; ++x) {
+            f16x2 y[4];
+            unit_f16<BITS>(&rg.v[x * KU], y);
+            const int q = NG == 1 ? 0 : (FS * x) / 64;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i] *= sc[q][i];
+            *reinterpret_cast<uint4 *>(buf + kKBytes + (vblk * D + vf + FS * x) * 16) =
+                make_uint4(u32(y[0]), u32(y[1]), u32(y[2]), u32(y[3]));
+        }
+        return ek;
+    };
+
+    // token of K row m: bits 2 and 3 exchanged, so that a lane's scores are 8 consecutive tokens twice
+    const int mtok = (m & 19) | ((m & 4) << 1) | ((m & 8) >> 1);
+    int tile = next_tile(ts);
+    int p0 = page_of(tile, 0), p1 = page_of(tile, 1);
+    int ek = 0, cur = 0;
+    __syncthreads();                                   // the queries have left LDS
+    if (tile < te) {
+        if (p0 >= 0 || p1 >= 0) {
+            fetch(tile, p0, p1);
+            ek = stage(tile, p0, p1, lds);
+        }
+    }
+    __syncthreads();
+    while (tile < te) {
+        const int nt = next_tile(tile + 1);
+        const int n0 = page_of(nt, 0), n1 = page_of(nt, 1);
+        const bool more = n0 >= 0 || n1 >= 0;
+        if (more) fetch(nt, n0, n1);
+        const int t0 = tile * kTile;
+        const uint8_t *buf = lds + cur * kBuf;
+        const bool any = active && (p0 >= 0 || p1 >= 0) && t0 < reach.hi_any &&
+                         (t0 + kTile > reach.lo_any || t0 < prefix);
+        if (any) {
+            if (enext > erun) {                        // the V unit grew
+                const float f = __builtin_ldexpf(1.f, erun - enext);
+#pragma unroll
+                for (int i = 0; i < NF; ++i) acc[i] *= f;
+                erun = enext;
+            }
+            const float kunit = kPost ? 1.f : __builtin_ldexpf(1.f, ek - 127 - (kTop - 15));
+            const float smul = mul * kunit, scap = cap_in * kunit;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int th = t0 + 32 * u;
+                f32x16 s;
+                if constexpr (kPost) {
+                    const float *ks = reinterpret_cast<const float *>(buf + kKBytes + kVBytes) + 32 * u + 8 * hh;
+#pragma unroll
+                    for (int q = 0; q < NG; ++q) {
+                        f32x16 x{};
+#pragma unroll
+                        for (int k = q * 4; k < q * 4 + 4; ++k) {
+                            const f16x8 kf = *reinterpret_cast<const f16x8 *>(buf + (2 * k + hh) * kKStride + (32 * u + mtok) * 16);
+#pragma unroll
+                            for (int p = 0; p < NP; ++p) x = mfma32(kf, qf[p][k], x);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4) {
+                            const float4 f = *reinterpret_cast<const float4 *>(ks + q * kTile + (i >> 3) * 16 + (i & 7));
+                            const float ff[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) s[i + y] = q == 0 ? x[i + y] * ff[y] : fmaf(x[i + y], ff[y], s[i + y]);
+                        }
+                    }
+                } else {
+                    s = f32x16{};
+#pragma unroll
+                    for (int k = 0; k < NK; ++k) {
+                        const f16x8 kf = *reinterpret_cast<const f16x8 *>(buf + (2 * k + hh) * kKStride + (32 * u + mtok) * 16);
+#pragma unroll
+                        for (int p = 0; p < NP; ++p) s = mfma32(kf, qf[p][k], s);
+                    }
+                }
+                if (a.cap > 0.f) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float x = __builtin_amdgcn_exp2f(-fabsf(s[i] * scap));
+                        s[i] = copysignf((1.f - x) * __builtin_amdgcn_rcpf(1.f + x), s[i]) * (a.cap * kLog2e);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) s[i] *= smul;
+                }
+                const bool here = (u ? p1 : p0) >= 0;
+                const bool full = here && th >= reach.lo_all && th + 32 <= reach.hi_all;
+                if (!full || a.slopes) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        int tp;
+                        const bool v = col.sees(a, th + (i >> 3) * 16 + 8 * hh + (i & 7), s0, n, base, len, prefix, &tp);
+                        s[i] -= col.slope * fabsf((float)(col.pos - tp));
+                        s[i] = v && here ? s[i] : neg_inf();
+                    }
+                }
+                float mx = s[0];
+#pragma unroll
+                for (int i = 1; i < 16; ++i) mx = fmaxf(mx, s[i]);
+                if (__any(mx > mrun + 8.f)) {
+                    mx = fmaxf(fmaxf(mx, __shfl_xor(mx, 32)), mrun);
+                    const float alpha = mx == mrun ? 1.f : __builtin_amdgcn_exp2f(mrun - mx);
+                    mrun = mx;
+                    lrun *= alpha;
+#pragma unroll
+                    for (int i = 0; i < NF; ++i) acc[i] *= alpha;
+                }
+                const float mu = mrun == neg_inf() ? 0.f : mrun;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    s[i] = __builtin_amdgcn_exp2f(s[i] - mu);
+                    lrun += s[i];
+                }
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const f16x8 pf = __builtin_bit_cast(
+                        f16x8, make_uint4(f16_pair(s[8 * t], s[8 * t + 1]), f16_pair(s[8 * t + 2], s[8 * t + 3]),
+                                          f16_pair(s[8 * t + 4], s[8 * t + 5]), f16_pair(s[8 * t + 6], s[8 * t + 7])));
+#pragma unroll
+                    for (int i = 0; i < NF; ++i) {
+                        const f16x8 vf8 = *reinterpret_cast<const f16x8 *>(
+                            buf + kKBytes + ((4 * u + 2 * t + hh) * D + 32 * i + m) * 16);
+                        acc[i] = mfma32(vf8, pf, acc[i]);
+                    }
+                }
+            }
+        }
+        if (more) ek = stage(nt, n0, n1, lds + (cur ^ 1) * kBuf);
+        __syncthreads();
+        cur ^= 1;
+        tile = nt;
+        p0 = n0;
+        p1 = n1;
+    }
+
+    // ---- rows out, 16 columns of the wave at a time
+    if (!active) return;
+    lrun += __shfl_xor(lrun, 32);
+    const float unit = __builtin_ldexpf(1.f, erun - 127 - (kTop - 15));
+    float *so = reinterpret_cast<float *>(lds) + wave * kOutCols * (D + 4);
+    constexpr int RL = D / 8, RW = 64 / RL;
+    const int r = lane / RL, j = lane % RL;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        if ((m >> 4) == half) {
+            float *row = so + (m & 15) * (D + 4);
+#pragma unroll
+            for (int i = 0; i < NF; ++i)
+#pragma unroll
+                for (int x = 0; x < 16; ++x) row[32 * i + 8 * (x >> 2) + 4 * hh + (x & 3)] = acc[i][x] * unit;
+            if (hh == 0) {
+                row[D] = mrun;
+                row[D + 1] = lrun;
+            }
+        }
+        wave_lds_sync();
+#pragma unroll
+        for (int it = 0; it < kOutCols / RW; ++it) {
+            const int cc = it * RW + r, cr = c0 + half * 16 + cc;
+            const float *row = so + cc * (D + 4);
+            const float4 u = *reinterpret_cast<const float4 *>(row + 8 * j), v = *reinterpret_cast<const float4 *>(row + 8 * j + 4);
+            float o[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+            const float mx = row[D], l = row[D + 1];
+            const int64_t qrow = s0 + cr / a.G;
+            const int head = h * a.G + cr % a.G;
+            if (a.splits == 1) finish_row<D, ROT>(a, qrow, head, j, o, mx, l, cr < ncol);
+            else if (cr < ncol) {
+                const int64_t rows = (int64_t)a.total * a.hq, at = split * rows + qrow * a.hq + head;
+                if (j == 0) {
+                    a.ws_ml[2 * at] = mx;
+                    a.ws_ml[2 * at + 1] = l;
+                }
+                if (mx != neg_inf()) {
+                    float4 *p = reinterpret_cast<float4 *>(a.ws_part + at * D + 8 * j);
+                    p[0] = make_float4(o[0], o[1], o[2], o[3]);
+                    p[1] = make_float4(o[4], o[5], o[6], o[7]);
+                }
+            }
+        }
+        wave_lds_sync();
+    }
+}
+
+template <int D, int BITS, bool ROT>
+static hipError_t wide_launch(const CacheAttnArgs &a, hipStream_t s) {
+    constexpr int NW = 4;
+    const int64_t ctiles = ((int64_t)a.max_q * a.G + 32 * NW - 1) / (32 * NW);
+    const int64_t grid = a.splits * ctiles * a.c.H * a.c.batch;
+    if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+    KTimeScope kts("k_cache_attn_wide", s);
+    hipLaunchKernelGGL((k_cache_attn_wide<D, BITS, ROT, NW>), dim3((unsigned)grid), dim3(64 * NW), 0, s, a, (int)ctiles);
+    return hipGetLastError();
+}
+template <int D>
+static hipError_t wide_d(const CacheAttnArgs &a, int bits, bool rotate, hipStream_t s) {
+    if (bits == 4) return rotate ? wide_launch<D, 4, true>(a, s) : wide_launch<D, 4, false>(a, s);
+    return rotate ? wide_launch<D, 8, true>(a, s) : wide_launch<D, 8, false>(a, s);
+}
+hipError_t launch_cache_attn_wide(const CacheAttnArgs &a, int d, int bits, bool rotate, hipStream_t s) {
+    return d == 128 ? wide_d<128>(a, bits, rotate, s) : wide_d<64>(a, bits, rotate, s);
+}
+
+}  // namespace jolt
