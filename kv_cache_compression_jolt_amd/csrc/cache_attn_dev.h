@@ -9,38 +9,60 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 
-// What a query column may see, in tokens: t >= first, and (t < prefix or
-// low <= t < hi); of a tree's slots those of its mask within the window.
+// bits e = 0..7 set where lo <= tb + e < hi (all three in 0 .. 2^30 or, for lo, above)
+__device__ __forceinline__ uint32_t range8(int tb, int lo, int hi) {
+    const int h = min(max(hi - tb, 0), 8), l = min(max(lo - tb, 0), 8);
+    return ((1u << h) - 1u) & (0xFFu << l);
+}
+
+// ancestors of a drafted token above itself
+__device__ __forceinline__ int tree_depth(uint64_t mask) {
+    const int n = (int)__popcll(mask);
+    return n > 0 ? n - 1 : 0;
+}
+
+// What a query column may see: tokens of [first, kept) and of [lo, hi), and of a
+// tree's slots (tokens from base on) those of its mask.
 struct Column {
-    int pos, low, first, hi;
+    int pos, first, kept, lo, hi;
     float slope;                          // slope * log2 e
     uint64_t mask;
 
-    // column c of KV head h in sequence b (valid: c < n G), whose rows start at s0
-    __device__ __forceinline__ Column(const CacheAttnArgs &a, int s0, int base, int h, int c, bool valid) {
+    // column c of KV head h in sequence b (valid: c < n G), whose n rows start at s0
+    __device__ __forceinline__ Column(const CacheAttnArgs &a, int s0, int n, int base, int len, int prefix, int h, int c,
+                                      bool valid) {
         const int i = valid ? c / a.G : 0;
         mask = 0;
         pos = base + i;
         if (a.tree) {
             mask = valid ? a.tree[s0 + i] : 0;
-            pos = base + max(__popcll(mask) - 1, 0);
+            pos = base + tree_depth(mask);
+            const int slots = min(min(n, kMaxKeep), len - base);
+            mask &= slots >= 64 ? ~0ull : (slots > 0 ? (1ull << slots) - 1ull : 0ull);
+            if (a.window > 0)             // a slot stands at the depth of its own path
+                for (int j = 0; j < min(n, kMaxKeep); ++j)
+                    if (tree_depth(a.tree[s0 + j]) <= pos - base - a.window) mask &= ~(1ull << j);
         }
-        first = valid && a.first ? a.first[s0 + i] : 0;
-        low = a.window > 0 ? pos - a.window + 1 : -0x7FFFFFFF;
-        hi = a.tree ? base : pos + 1;
+        first = valid && a.first ? max(a.first[s0 + i], 0) : 0;
+        kept = a.tree ? min(prefix, base) : min(prefix, len);
+        lo = max(a.window > 0 ? pos - a.window + 1 : 0, first);
+        hi = a.tree ? base : min(pos + 1, len);
         slope = a.slopes ? a.slopes[h * a.G + (valid ? c % a.G : 0)] * kLog2e : 0.f;
     }
-    // whether token t is visible; *tp: its position
-    __device__ __forceinline__ bool sees(const CacheAttnArgs &a, int t, int s0, int n, int base, int len, int prefix,
-                                         int *tp) const {
-        *tp = t;
-        if (a.tree && t >= base) {
-            const int slot = t - base;
-            const bool in = slot < n && slot < kMaxKeep && t < len;
-            *tp = base + (in ? max(__popcll(a.tree[s0 + slot]) - 1, 0) : 0);
-            return in && ((mask >> (slot & 63)) & 1) && *tp >= low;
+    // which of tokens tb .. tb + 7 are visible
+    __device__ __forceinline__ uint32_t sees8(bool tree, int base, int tb) const {
+        uint32_t v = range8(tb, first, kept) | range8(tb, lo, hi);
+        if (tree && tb + 8 > base) {
+            const int s = tb - base;
+            if (s < 64) v |= (uint32_t)(s >= 0 ? mask >> s : mask << -s) & 0xFFu;
         }
-        return t < len && t >= first && (t < prefix || (t >= low && t < hi));
+        return v;
+    }
+    // |position of this row - position of token t|
+    __device__ __forceinline__ float distance(const CacheAttnArgs &a, int t, int s0, int n, int base) const {
+        int tp = t;
+        if (a.tree && t >= base && t - base < n) tp = base + tree_depth(a.tree[s0 + t - base]);
+        return fabsf((float)(pos - tp));
     }
 };
 
@@ -49,10 +71,9 @@ struct Column {
 struct Reach {
     int lo_any, hi_any, lo_all, hi_all, first_any;
     __device__ __forceinline__ Reach(const Column &c, bool valid) {
-        const int lo = max(c.low, c.first);
-        lo_any = valid ? lo : 0x7FFFFFFF;
+        lo_any = valid ? c.lo : 0x7FFFFFFF;
         hi_any = valid ? c.hi : 0;
-        lo_all = valid ? lo : -0x7FFFFFFF;
+        lo_all = valid ? c.lo : -0x7FFFFFFF;
         hi_all = valid ? c.hi : 0x7FFFFFFF;
         first_any = valid ? c.first : 0x7FFFFFFF;
     }

@@ -207,7 +207,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_cache_attn(CacheAttnArgs a, int
     // ---- what the columns see
     const int c = ct * kCols + m, ncol = n * a.G;
     const bool cv = c < ncol;
-    const Column col(a, s0, base, h, c, cv);
+    const Column col(a, s0, n, base, len, prefix, h, c, cv);
     Reach reach(col, cv);
     reach.join<16>();
     reach.clip(a, len, prefix);
@@ -276,17 +276,15 @@ __global__ __launch_bounds__(64 * kWaves) void k_cache_attn(CacheAttnArgs a, int
                 for (int e = 0; e < 8; ++e) s[e] *= mul;
             }
             const bool full = t0 >= lo_all && t0 + 32 <= hi_all;
-            uint32_t vis = 0xFFu;
-            if (!full || a.slopes) {
-                vis = 0;
+            if (a.slopes) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    int tp;
-                    const bool v = col.sees(a, t0 + 8 * g + e, s0, n, base, len, prefix, &tp);
-                    vis |= (uint32_t)v << e;
-                    s[e] -= col.slope * fabsf((float)(col.pos - tp));
-                    s[e] = v ? s[e] : neg_inf();
-                }
+                for (int e = 0; e < 8; ++e) s[e] -= col.slope * col.distance(a, t0 + 8 * g + e, s0, n, base);
+            }
+            uint32_t vis = 0xFFu;
+            if (!full) {
+                vis = col.sees8(a.tree != nullptr, base, t0 + 8 * g);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s[e] = (vis >> e) & 1 ? s[e] : neg_inf();
             }
             float mx = s[0];
 #pragma unroll

@@ -202,7 +202,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
     // ---- what the wave's columns see, and the workgroup's range of tiles
     const int c = c0 + m;
     const bool cv = c < ncol;
-    const Column col(a, s0, base, h, c, cv);
+    const Column col(a, s0, n, base, len, prefix, h, c, cv);
     Reach reach(col, cv);
     reach.join<32>();
     reach.clip(a, len, prefix);
@@ -388,10 +388,9 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
             }
             const float kunit = kPost ? 1.f : __builtin_ldexpf(1.f, ek - 127 - (kTop - 15));
             const float smul = mul * kunit, scap = cap_in * kunit;
+            f32x16 s[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const int th = t0 + 32 * u;
-                f32x16 s;
                 if constexpr (kPost) {
                     const float *ks = reinterpret_cast<const float *>(buf + kKBytes + kVBytes) + 32 * u + 8 * hh;
 #pragma unroll
@@ -408,69 +407,87 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
                             const float4 f = *reinterpret_cast<const float4 *>(ks + q * kTile + (i >> 3) * 16 + (i & 7));
                             const float ff[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-                            for (int y = 0; y < 4; ++y) s[i + y] = q == 0 ? x[i + y] * ff[y] : fmaf(x[i + y], ff[y], s[i + y]);
+                            for (int y = 0; y < 4; ++y)
+                                s[u][i + y] = q == 0 ? x[i + y] * ff[y] : fmaf(x[i + y], ff[y], s[u][i + y]);
                         }
                     }
                 } else {
-                    s = f32x16{};
+                    s[u] = f32x16{};
 #pragma unroll
                     for (int k = 0; k < NK; ++k) {
                         const f16x8 kf = *reinterpret_cast<const f16x8 *>(buf + (2 * k + hh) * kKStride + (32 * u + mtok) * 16);
 #pragma unroll
-                        for (int p = 0; p < NP; ++p) s = mfma32(kf, qf[p][k], s);
-                    }
-                }
-                if (a.cap > 0.f) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float x = __builtin_amdgcn_exp2f(-fabsf(s[i] * scap));
-                        s[i] = copysignf((1.f - x) * __builtin_amdgcn_rcpf(1.f + x), s[i]) * (a.cap * kLog2e);
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) s[i] *= smul;
-                }
-                const bool here = (u ? p1 : p0) >= 0;
-                const bool full = here && th >= reach.lo_all && th + 32 <= reach.hi_all;
-                if (!full || a.slopes) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        int tp;
-                        const bool v = col.sees(a, th + (i >> 3) * 16 + 8 * hh + (i & 7), s0, n, base, len, prefix, &tp);
-                        s[i] -= col.slope * fabsf((float)(col.pos - tp));
-                        s[i] = v && here ? s[i] : neg_inf();
-                    }
-                }
-                float mx = s[0];
-#pragma unroll
-                for (int i = 1; i < 16; ++i) mx = fmaxf(mx, s[i]);
-                if (__any(mx > mrun + 8.f)) {
-                    mx = fmaxf(fmaxf(mx, __shfl_xor(mx, 32)), mrun);
-                    const float alpha = mx == mrun ? 1.f : __builtin_amdgcn_exp2f(mrun - mx);
-                    mrun = mx;
-                    lrun *= alpha;
-#pragma unroll
-                    for (int i = 0; i < NF; ++i) acc[i] *= alpha;
-                }
-                const float mu = mrun == neg_inf() ? 0.f : mrun;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    s[i] = __builtin_amdgcn_exp2f(s[i] - mu);
-                    lrun += s[i];
-                }
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const f16x8 pf = __builtin_bit_cast(
-                        f16x8, make_uint4(f16_pair(s[8 * t], s[8 * t + 1]), f16_pair(s[8 * t + 2], s[8 * t + 3]),
-                                          f16_pair(s[8 * t + 4], s[8 * t + 5]), f16_pair(s[8 * t + 6], s[8 * t + 7])));
-#pragma unroll
-                    for (int i = 0; i < NF; ++i) {
-                        const f16x8 vf8 = *reinterpret_cast<const f16x8 *>(
-                            buf + kKBytes + ((4 * u + 2 * t + hh) * D + 32 * i + m) * 16);
-                        acc[i] = mfma32(vf8, pf, acc[i]);
+                        for (int p = 0; p < NP; ++p) s[u] = mfma32(kf, qf[p][k], s[u]);
                     }
                 }
             }
+            // scores in units of smul (log2 e times the scale's factors), or, where the
+            // terms are not linear, in log2 units already
+            float unit = smul;
+            if (a.cap > 0.f) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float x = __builtin_amdgcn_exp2f(-fabsf(s[u][i] * scap));
+                        s[u][i] = copysignf((1.f - x) * __builtin_amdgcn_rcpf(1.f + x), s[u][i]) * (a.cap * kLog2e);
+                    }
+                unit = 1.f;
+            }
+            if (a.slopes) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        s[u][i] = s[u][i] * unit - col.slope * col.distance(a, t0 + 32 * u + (i >> 3) * 16 + 8 * hh + (i & 7), s0, n, base);
+                unit = 1.f;
+            }
+            const bool full = p0 >= 0 && p1 >= 0 && t0 >= reach.lo_all && t0 + kTile <= reach.hi_all;
+            if (!full) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        uint32_t vis = col.sees8(a.tree != nullptr, base, t0 + 32 * u + 16 * x + 8 * hh);
+                        if ((u ? p1 : p0) < 0) vis = 0;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) s[u][8 * x + e] = (vis >> e) & 1 ? s[u][8 * x + e] : neg_inf();
+                    }
+            }
+            float mx = s[0][0];
+#pragma unroll
+            for (int i = 1; i < 16; ++i) mx = fmaxf(mx, s[0][i]);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[1][i]);
+            mx *= unit;
+            if (__any(mx > mrun + 8.f)) {
+                mx = fmaxf(fmaxf(mx, __shfl_xor(mx, 32)), mrun);
+                const float alpha = mx == mrun ? 1.f : __builtin_amdgcn_exp2f(mrun - mx);
+                mrun = mx;
+                lrun *= alpha;
+#pragma unroll
+                for (int i = 0; i < NF; ++i) acc[i] *= alpha;
+            }
+            const float mu = mrun == neg_inf() ? 0.f : -mrun;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    float p[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        p[e] = __builtin_amdgcn_exp2f(fmaf(s[u][8 * x + e], unit, mu));
+                        lrun += p[e];
+                    }
+                    const f16x8 pf = __builtin_bit_cast(f16x8, make_uint4(f16_pair(p[0], p[1]), f16_pair(p[2], p[3]),
+                                                                          f16_pair(p[4], p[5]), f16_pair(p[6], p[7])));
+#pragma unroll
+                    for (int i = 0; i < NF; ++i) {
+                        const f16x8 vf8 = *reinterpret_cast<const f16x8 *>(
+                            buf + kKBytes + ((4 * u + 2 * x + hh) * D + 32 * i + m) * 16);
+                        acc[i] = mfma32(vf8, pf, acc[i]);
+                    }
+                }
         }
         if (more) ek = stage(nt, n0, n1, lds + (cur ^ 1) * kBuf);
         __syncthreads();
@@ -483,7 +500,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
     // ---- rows out, 16 columns of the wave at a time
     if (!active) return;
     lrun += __shfl_xor(lrun, 32);
-    const float unit = __builtin_ldexpf(1.f, erun - 127 - (kTop - 15));
+    const float vunit = __builtin_ldexpf(1.f, erun - 127 - (kTop - 15));
     float *so = reinterpret_cast<float *>(lds) + wave * kOutCols * (D + 4);
     constexpr int RL = D / 8, RW = 64 / RL;
     const int r = lane / RL, j = lane % RL;
@@ -494,7 +511,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
 #pragma unroll
             for (int i = 0; i < NF; ++i)
 #pragma unroll
-                for (int x = 0; x < 16; ++x) row[32 * i + 8 * (x >> 2) + 4 * hh + (x & 3)] = acc[i][x] * unit;
+                for (int x = 0; x < 16; ++x) row[32 * i + 8 * (x >> 2) + 4 * hh + (x & 3)] = acc[i][x] * vunit;
             if (hh == 0) {
                 row[D] = mrun;
                 row[D + 1] = lrun;
