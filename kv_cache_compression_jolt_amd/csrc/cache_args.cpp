@@ -81,7 +81,7 @@ AttnPlan cache_attn_plan(const jolt_cache &c, int batch, int64_t total, int max_
     AttnPlan p{};
     const int64_t cols = (int64_t)max_q * (q_heads / c.H);
     p.wide = cols > 32;
-    const int64_t per = p.wide ? 128 : 16, want = p.wide ? 512 : 1024, least = p.wide ? 512 : 256;
+    const int64_t per = p.wide ? 256 : 16, want = p.wide ? 256 : 1024, least = p.wide ? 512 : 256;
     const int64_t tiles = std::max<int64_t>(1, (int64_t)batch * c.H * ((cols + per - 1) / per));
     p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(max_len / least, want / tiles));
     if (p.splits > 1) {

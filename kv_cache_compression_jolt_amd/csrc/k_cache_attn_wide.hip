@@ -27,7 +27,7 @@ namespace {
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-typedef short s16x2 __attribute__((ext_vector_type(2)));
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kTile = 64;                              // tokens of a tile
 
@@ -42,67 +42,60 @@ __device__ __forceinline__ f16x2 h2(uint32_t w) { return __builtin_bit_cast(f16x
 __device__ __forceinline__ uint32_t u32(f16x2 v) { return __builtin_bit_cast(uint32_t, v); }
 
 // a unit of 8 codes as signed fp16 integers, exact.  4 bits: a nibble under the
-// exponent of 1024 is 1024 + u, or 1024 + 16 u from the next nibble up.
+// exponent of 1024 is 1024 + u, or 1024 + 16 u from the next nibble up.  `magic`
+// is 0x64006400 in a vector register (with the mask in a scalar one, an and-or
+// is one instruction).
 template <int BITS>
-__device__ __forceinline__ void unit_f16(const uint32_t *w, f16x2 (&x)[4]) {
+__device__ __forceinline__ void unit_f16(const uint32_t *w, uint32_t magic, f16x2 (&x)[4]) {
     if constexpr (BITS == 4) {
         const f16x2 c0 = {(_Float16)-1032.f, (_Float16)-1032.f}, c1 = {(_Float16)-72.f, (_Float16)-72.f};
         const f16x2 r = {(_Float16)0.0625f, (_Float16)0.0625f};
+        uint32_t m0 = 0x000F000Fu, m1 = 0x00F000F0u;
+        asm("" : "+s"(m0), "+s"(m1));
         const uint32_t a = w[0], b = a >> 8;
-        x[0] = h2((a & 0x000F000Fu) | 0x64006400u) + c0;
-        x[1] = __builtin_elementwise_fma(h2((a & 0x00F000F0u) | 0x64006400u), r, c1);
-        x[2] = h2((b & 0x000F000Fu) | 0x64006400u) + c0;
-        x[3] = __builtin_elementwise_fma(h2((b & 0x00F000F0u) | 0x64006400u), r, c1);
+        x[0] = h2((a & m0) | magic) + c0;
+        x[1] = __builtin_elementwise_fma(h2((a & m1) | magic), r, c1);
+        x[2] = h2((b & m0) | magic) + c0;
+        x[3] = __builtin_elementwise_fma(h2((b & m1) | magic), r, c1);
     } else {
         const f16x2 c0 = {(_Float16)-1152.f, (_Float16)-1152.f};
 #pragma unroll
         for (int i = 0; i < 4; ++i)                    // bytes 2 i, 2 i + 1 under the exponent of 1024
-            x[i] = h2(__builtin_amdgcn_perm(w[i >> 1], 0x64646464u, (i & 1) ? 0x00070006u : 0x00050004u)) + c0;
+            x[i] = h2(__builtin_amdgcn_perm(w[i >> 1], magic, (i & 1) ? 0x01070106u : 0x01050104u)) + c0;
     }
 }
 
-// bf16 scales (two) as fp16 with field exponent e + shift; below the range: 0
-__device__ __forceinline__ f16x2 scale_f16(uint32_t two, int shift) {
-    s16x2 v = __builtin_bit_cast(s16x2, two);
-    const short d = (short)(shift << 7);
-    v += s16x2{d, d};
-    v = __builtin_elementwise_max(v, s16x2{0, 0});
-    v <<= s16x2{3, 3};
-    return __builtin_bit_cast(f16x2, v);
+// two bf16 scales as fp16 with their exponent fields lowered by `down` (of both
+// halves, at bit 7); what falls below the range becomes 0
+__device__ __forceinline__ f16x2 scale_f16(uint32_t two, uint32_t down) {
+    const u16x2 v = __builtin_elementwise_sub_sat(__builtin_bit_cast(u16x2, two), __builtin_bit_cast(u16x2, down));
+    return __builtin_bit_cast(f16x2, v << u16x2{3, 3});
+}
+__device__ __forceinline__ uint32_t pk_umax(uint32_t a, uint32_t b) {
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
+}
+template <int Ctrl>
+__device__ __forceinline__ uint32_t dpp_u(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, Ctrl, 0xF, 0xF, false);
 }
 
-__device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
-    v = group_umax<16>(v);
-    const int i = (int)v;
-    const uint32_t a = max((uint32_t)__builtin_amdgcn_readlane(i, 0), (uint32_t)__builtin_amdgcn_readlane(i, 16));
-    const uint32_t b = max((uint32_t)__builtin_amdgcn_readlane(i, 32), (uint32_t)__builtin_amdgcn_readlane(i, 48));
-    return max(a, b);
-}
-
-// largest finite exponent field of two packed bf16 scales (sign clear)
-__device__ __forceinline__ uint32_t max_exponent(uint32_t two) {
-    const uint32_t a = (two >> 7) & 0xFFu, b = (two >> 23) & 0xFFu;
-    return max(a == 255u ? 0u : a, b == 255u ? 0u : b);
-}
-
-// One thread's share of a tile: UPT units of K and of V, the scales they need,
-// and the tile's scales for their largest exponent (two tokens of a group to a
-// lane: lanes 0..31 group 0, 32..63 group 1).
+// One thread's share of a tile: UPT units of K and of V and the scales they
+// need; all: two scales a lane of each half of the tile (lanes 0..31 K, 32..63
+// V), for the tile's largest.
 template <int D, int BITS, int NT>
 struct TileRegs {
     static constexpr int kU = BITS / 4;                // dwords of a unit
     static constexpr int UPT = kTile * D / 8 / NT;
     static constexpr int FS = NT / 8;                  // a thread's V features: f, f + FS, ...
-    uint32_t k[UPT * kU], v[UPT * kU], vs[D / 64][4];
-    uint32_t allk, allv;
-    uint16_t ks[D / 64], vbad;
+    uint32_t k[UPT * kU], v[UPT * kU], vs[D / 64][4], all[2];
+    uint16_t ks[D / 64];
 };
 
 }  // namespace
 
 template <int D, int BITS, bool ROT, int NW>
 __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a, int ctiles) {
-    constexpr int NT = 64 * NW, NK = D / 16, NF = D / 32, NG = D / 64, NP = ROT ? 2 : 1;
+    constexpr int NT = 64 * NW, NK = D / 16, NF = D / 32, NG = D / 64;
     constexpr bool kPost = BITS == 8;                  // K scales multiply the scores
     constexpr int kTop = BITS == 4 ? 27 : 23;          // fp16 exponent field of the largest scale
     constexpr int kKStride = kTile * 16 + 32;          // bytes of a K chunk (8 features of 64 tokens), padded
@@ -111,7 +104,10 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
     constexpr int kBuf = kKBytes + kVBytes + kSBytes;
     constexpr int kOutCols = 16;                       // columns of a wave that leave through LDS together
     constexpr int kOut = NW * kOutCols * (D + 4) * 4;
-    __shared__ __align__(16) uint8_t lds[2 * kBuf > kOut ? 2 * kBuf : kOut];
+    constexpr int kMain = 2 * kBuf > kOut ? 2 * kBuf : kOut;
+    constexpr bool kLo = ROT;                          // the queries' second parts stay in LDS: a lane's own fragments
+    __shared__ __align__(16) uint8_t lds[kMain + (kLo ? NW * NK * 1024 : 0)];
+    uint8_t *const qlo = lds + kMain + (threadIdx.x >> 6) * (NK * 1024) + (threadIdx.x & 63) * 16;
     __shared__ int reach_all[NW][3];
     typedef TileRegs<D, BITS, NT> Regs;
     constexpr int UPT = Regs::UPT, KU = Regs::kU, FS = Regs::FS;
@@ -134,7 +130,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
     const bool active = c0 < ncol;
 
     // ---- queries: 16 columns of the wave at a time through its part of LDS
-    f16x8 qf[NP][NK];
+    f16x8 qf[NK];
     float qmul = 0.f;                                  // what the column's scores are multiplied with
     {
         float *sq = reinterpret_cast<float *>(lds) + wave * kOutCols * (D + 4);
@@ -191,8 +187,8 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
                         hi[i] = f16_pair(x0, x1);
                         lo[i] = f16_pair(x0 - (float)h2(hi[i])[0], x1 - (float)h2(hi[i])[1]);
                     }
-                    qf[0][k] = __builtin_bit_cast(f16x8, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-                    if constexpr (ROT) qf[NP - 1][k] = __builtin_bit_cast(f16x8, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+                    qf[k] = __builtin_bit_cast(f16x8, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+                    if constexpr (kLo) *reinterpret_cast<uint4 *>(qlo + k * 1024) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
             }
             wave_lds_sync();
@@ -240,21 +236,26 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
     auto page_of = [&](int t, int half) -> int {
         return t < te ? cache_page(a.c, b, t * kTile + 32 * half) : -1;
     };
-    // units of K: consecutive ones of a row; units of V: features f, f + FS, .. of a block of 8 tokens
+    // units of K: consecutive ones of a row; units of V: features f, f + FS, .. of
+    // a block of 8 tokens.  The first half of the waves has the tile's first 32
+    // tokens, so that a wave reads one page.
     const int kidx = tid * UPT, ktok = kidx / (D / 8), ku0 = kidx % (D / 8);
     const int vblk = tid / FS, vf = tid % FS;
+    const bool second = __builtin_amdgcn_readfirstlane(wave) >= NW / 2;
+    const uint32_t koff = (ktok & 31) * (D * BITS / 8) + ku0 * (4 * KU), voff = (vblk & 3) * (D * BITS) + vf * (4 * KU);
+    const uint32_t all_off = (uint32_t)(hh ? pl.v_scales : pl.k_scales) + ((NG == 2 ? m >> 4 : 0) * P + 2 * (m & 15)) * 2;
     Regs rg;
     auto fetch = [&](int t, int p0, int p1) {
         const int t0 = t * kTile;
-        // tokens without a page read page 0 of the pool's first head (never used: their scales count as 0);
-        // a call with pages == 0 has no valid page and fetches nothing
+        // a half without a page reads page 0 (never used: its scales count as 0); a
+        // call with pages == 0 has no valid page and fetches nothing
         const uint8_t *b0 = a.c.pool + (p0 >= 0 ? cache_block_offset(a.c, p0, h) : 0);
         const uint8_t *b1 = a.c.pool + (p1 >= 0 ? cache_block_offset(a.c, p1, h) : 0);
         const int i0 = t0 & (P - 1), i1 = (t0 + 32) & (P - 1);
+        const uint8_t *bw = second ? b1 : b0;
+        const int iw = second ? i1 : i0;
         {
-            const uint8_t *kb = ktok < 32 ? b0 : b1;
-            const int tin = ktok < 32 ? i0 + ktok : i1 + ktok - 32;
-            const uint8_t *p = kb + tin * (D * BITS / 8) + ku0 * (4 * KU);
+            const uint8_t *p = bw + iw * (D * BITS / 8) + koff;
             constexpr int N = UPT * KU;
             if constexpr (N == 1) rg.k[0] = *reinterpret_cast<const uint32_t *>(p);
             else if constexpr (N == 2) {
@@ -268,86 +269,119 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
                 }
             }
 #pragma unroll
-            for (int q = 0; q < NG; ++q) rg.ks[q] = reinterpret_cast<const uint16_t *>(kb + pl.k_scales)[q * P + tin];
-            rg.vbad = reinterpret_cast<const uint16_t *>(kb + pl.v_scales)[tin];
+            for (int q = 0; q < NG; ++q)
+                rg.ks[q] = *reinterpret_cast<const uint16_t *>(bw + pl.k_scales + (q * P + iw) * 2 + (uint32_t)(ktok & 31) * 2u);
         }
         {
-            const uint8_t *vb = vblk < 4 ? b0 : b1;
-            const int tin = vblk < 4 ? i0 + 8 * vblk : i1 + 8 * vblk - 32;
-            const uint8_t *p = vb + pl.v_codes + (tin >> 3) * (D * BITS);
+            const uint8_t *p = bw + pl.v_codes + (iw >> 3) * (D * BITS) + voff;
 #pragma unroll
             for (int x = 0; x < UPT; ++x) {
-                if constexpr (KU == 1) rg.v[x] = reinterpret_cast<const uint32_t *>(p)[vf + FS * x];
+                if constexpr (KU == 1) rg.v[x] = *reinterpret_cast<const uint32_t *>(p + FS * x * 4);
                 else {
-                    const uint2 v = reinterpret_cast<const uint2 *>(p)[vf + FS * x];
+                    const uint2 v = *reinterpret_cast<const uint2 *>(p + FS * x * 8);
                     rg.v[2 * x] = v.x; rg.v[2 * x + 1] = v.y;
                 }
             }
 #pragma unroll
             for (int q = 0; q < NG; ++q) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(vb + pl.v_scales + (q * P + tin) * 2);
+                const uint4 v = *reinterpret_cast<const uint4 *>(bw + pl.v_scales + (q * P + iw) * 2 + (uint32_t)(vblk & 3) * 16u);
                 rg.vs[q][0] = v.x; rg.vs[q][1] = v.y; rg.vs[q][2] = v.z; rg.vs[q][3] = v.w;
             }
         }
-        {
-            const int q = NG == 2 ? hh : 0;
-            const uint8_t *sb = m < 16 ? b0 : b1;
-            const int tin = m < 16 ? i0 + 2 * m : i1 + 2 * m - 32;
-            rg.allk = *reinterpret_cast<const uint32_t *>(sb + pl.k_scales + (q * P + tin) * 2);
-            rg.allv = *reinterpret_cast<const uint32_t *>(sb + pl.v_scales + (q * P + tin) * 2);
-        }
+        rg.all[0] = *reinterpret_cast<const uint32_t *>(b0 + i0 * 2 + all_off);
+        rg.all[1] = *reinterpret_cast<const uint32_t *>(b1 + i1 * 2 + all_off);
     };
     // registers -> LDS; returns the exponent field of the tile's K unit, and raises enext
     int enext = kTop;                                  // (the floor keeps a zero scale zero)
+    uint32_t magic = 0x64006400u;
+    asm("" : "+v"(magic));
     auto stage = [&](int t, int p0, int p1, uint8_t *buf) -> int {
         const int t0 = t * kTile;
         const int lim0 = p0 >= 0 ? len : 0, lim1 = p1 >= 0 ? len : 0;      // tokens below these count, by half
-        // two tokens a lane: keep those that count
-        const int te0 = t0 + 2 * m, lim = m < 16 ? lim0 : lim1;
-        const uint32_t keep = (te0 < lim ? 0xFFFFu : 0u) | (te0 + 1 < lim ? 0xFFFF0000u : 0u);
-        const int ek = kPost ? 0 : max((int)wave_umax(max_exponent(rg.allk & keep)), kTop);
-        enext = max(enext, (int)wave_umax(max_exponent(rg.allv & keep)));
-        {
-            const bool on = t0 + ktok < (ktok < 32 ? lim0 : lim1);
-            const bool bad = (rg.vbad & 0x7F80u) == 0x7F80u || (rg.ks[0] & 0x7F80u) == 0x7F80u;
-#pragma unroll
-            for (int x = 0; x < UPT; ++x) {
-                const int u = ku0 + x, g = u / (D / 32), kk = u % (D / 32);
-                f16x2 y[4];
-                unit_f16<BITS>(&rg.k[x * KU], y);
-                if constexpr (!kPost) {
-                    const uint32_t s = on ? rg.ks[kk / 2] : 0u;
-                    f16x2 sc = scale_f16(s | (s << 16), kTop - ek);
-                    if (bad && on) sc = h2(0x7E007E00u);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) y[i] *= sc;
-                }
-                *reinterpret_cast<uint4 *>(buf + (4 * kk + g) * kKStride + ktok * 16) =
-                    make_uint4(u32(y[0]), u32(y[1]), u32(y[2]), u32(y[3]));
-            }
-            if constexpr (kPost) {
-                if (ku0 == 0)
-#pragma unroll
-                    for (int q = 0; q < NG; ++q)
-                        reinterpret_cast<float *>(buf + kKBytes + kVBytes)[q * kTile + ktok] =
-                            !on ? 0.f : (bad ? __builtin_nanf("") : bf16_to_f32(rg.ks[q]));
-            }
+        const bool whole = t0 + kTile <= min(lim0, lim1);
+        uint32_t all0 = rg.all[0], all1 = rg.all[1];
+        if (!whole) {
+            const int ta = t0 + 2 * (m & 15), tb = ta + 32;
+            all0 &= (ta < lim0 ? 0xFFFFu : 0u) | (ta + 1 < lim0 ? 0xFFFF0000u : 0u);
+            all1 &= (tb < lim1 ? 0xFFFFu : 0u) | (tb + 1 < lim1 ? 0xFFFF0000u : 0u);
         }
-        const int tv = t0 + 8 * vblk, vlim = vblk < 4 ? lim0 : lim1;
+        // largest scale of K (lanes 0..31) and V (32..63): rows of 16, then the second row of each half
+        uint32_t x = pk_umax(all0, all1);
+        x = pk_umax(x, dpp_u<kDppXor1>(x));
+        x = pk_umax(x, dpp_u<kDppXor2>(x));
+        x = pk_umax(x, dpp_u<kDppHalfMirror>(x));
+        x = pk_umax(x, dpp_u<kDppMirror>(x));
+        x = pk_umax(x, dpp_u<kDppRowBcast15>(x));
+        const uint32_t xk = (uint32_t)__builtin_amdgcn_readlane((int)x, 31), xv = (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
+        int ek = (int)(max(xk & 0xFFFFu, xk >> 16) >> 7), ev = (int)(max(xv & 0xFFFFu, xv >> 16) >> 7);
+        const bool clean = whole && ek < 255 && ev < 255;
+        uint32_t kbad = 0;
+        if (!clean) {
+            // a tile with a last token, a missing half or a NaN scale inside: scales
+            // that do not count become 0, and a NaN of K or V goes into the K row
+            auto finite = [&](uint32_t two, int tt, int lim) -> uint32_t {
+                if (tt >= lim || (two & 0x7F80u) == 0x7F80u) two &= 0xFFFF0000u;
+                if (tt + 1 >= lim || (two & 0x7F800000u) == 0x7F800000u) two &= 0x0000FFFFu;
+                return two;
+            };
+            x = pk_umax(finite(all0, 0, 2), finite(all1, 0, 2));
+            x = pk_umax(x, dpp_u<kDppXor1>(x));
+            x = pk_umax(x, dpp_u<kDppXor2>(x));
+            x = pk_umax(x, dpp_u<kDppHalfMirror>(x));
+            x = pk_umax(x, dpp_u<kDppMirror>(x));
+            x = pk_umax(x, dpp_u<kDppRowBcast15>(x));
+            const uint32_t yk = (uint32_t)__builtin_amdgcn_readlane((int)x, 31), yv = (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
+            ek = (int)(max(yk & 0xFFFFu, yk >> 16) >> 7);
+            ev = (int)(max(yv & 0xFFFFu, yv >> 16) >> 7);
+            const int limw = second ? lim1 : lim0, tk = t0 + ktok, tv = t0 + 8 * vblk;
+            const int pw = second ? p1 : p0;
+            if (tk < limw) {                           // limw > 0: the half has a page
+                const uint8_t *sv = a.c.pool + cache_block_offset(a.c, max(pw, 0), h) + pl.v_scales;
+                const uint32_t vs0 = reinterpret_cast<const uint16_t *>(sv)[tk & (P - 1)];
+                if ((rg.ks[0] & 0x7F80u) == 0x7F80u || (vs0 & 0x7F80u) == 0x7F80u) kbad = 0x7E007E00u;
+            } else {
+#pragma unroll
+                for (int q = 0; q < NG; ++q) rg.ks[q] = 0;
+            }
+#pragma unroll
+            for (int q = 0; q < NG; ++q)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) rg.vs[q][i] = finite(rg.vs[q][i], tv + 2 * i, limw);
+        }
+        ek = max(ek, kTop);
+        enext = max(enext, ev);
+        const uint32_t kdown = (uint32_t)(ek - kTop) * 0x00800080u, vdown = (uint32_t)(enext - kTop) * 0x00800080u;
+#pragma unroll
+        for (int x = 0; x < UPT; ++x) {
+            const int u = ku0 + x, g = u / (D / 32), kk = u % (D / 32);
+            f16x2 y[4];
+            unit_f16<BITS>(&rg.k[x * KU], magic, y);
+            if constexpr (!kPost) {
+                // kk runs from ku0 % (D/32) on: with D / 32 <= 4 its group is known or one of two
+                const uint32_t s = NG == 1 ? rg.ks[0] : (kk & 2 ? rg.ks[NG - 1] : rg.ks[0]);
+                const f16x2 sc = h2(u32(scale_f16(s | (s << 16), kdown)) | kbad);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[i] *= sc;
+            }
+            *reinterpret_cast<uint4 *>(buf + (4 * kk + g) * kKStride + ktok * 16) =
+                make_uint4(u32(y[0]), u32(y[1]), u32(y[2]), u32(y[3]));
+        }
+        if constexpr (kPost) {
+            if (ku0 == 0)
+#pragma unroll
+                for (int q = 0; q < NG; ++q)
+                    reinterpret_cast<float *>(buf + kKBytes + kVBytes)[q * kTile + ktok] =
+                        kbad ? __builtin_nanf("") : bf16_to_f32(rg.ks[q]);
+        }
         f16x2 sc[NG][4];
 #pragma unroll
         for (int q = 0; q < NG; ++q)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t s = rg.vs[q][i];
-                if (tv + 2 * i >= vlim || (s & 0x7F80u) == 0x7F80u) s &= 0xFFFF0000u;
-                if (tv + 2 * i + 1 >= vlim || (s & 0x7F800000u) == 0x7F800000u) s &= 0x0000FFFFu;
-                sc[q][i] = scale_f16(s, kTop - enext);
-            }
+            for (int i = 0; i < 4; ++i) sc[q][i] = scale_f16(rg.vs[q][i], vdown);
 #pragma unroll
         for (int x = 0; x < UPT; ++x) {
             f16x2 y[4];
-            unit_f16<BITS>(&rg.v[x * KU], y);
+            unit_f16<BITS>(&rg.v[x * KU], magic, y);
             const int q = NG == 1 ? 0 : (FS * x) / 64;
 #pragma unroll
             for (int i = 0; i < 4; ++i) y[i] *= sc[q][i];
@@ -386,40 +420,46 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
                 for (int i = 0; i < NF; ++i) acc[i] *= f;
                 erun = enext;
             }
-            const float kunit = kPost ? 1.f : __builtin_ldexpf(1.f, ek - 127 - (kTop - 15));
+            const float kunit = kPost ? 1.f : __builtin_ldexpf(1.f, ek - 127 - (kTop - 15));   // 2^E
             const float smul = mul * kunit, scap = cap_in * kunit;
             f32x16 s[2];
+            // s[u] += K rows of half u times the queries, features 16 k0 .. 16 (k1) - 1
+            auto products = [&](f32x16 (&x)[2], int k0, int k1) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                if constexpr (kPost) {
-                    const float *ks = reinterpret_cast<const float *>(buf + kKBytes + kVBytes) + 32 * u + 8 * hh;
+                for (int k = k0; k < k1; ++k) {
+                    f16x8 kf[2];
 #pragma unroll
-                    for (int q = 0; q < NG; ++q) {
-                        f32x16 x{};
+                    for (int u = 0; u < 2; ++u)
+                        kf[u] = *reinterpret_cast<const f16x8 *>(buf + (2 * k + hh) * kKStride + (32 * u + mtok) * 16);
 #pragma unroll
-                        for (int k = q * 4; k < q * 4 + 4; ++k) {
-                            const f16x8 kf = *reinterpret_cast<const f16x8 *>(buf + (2 * k + hh) * kKStride + (32 * u + mtok) * 16);
+                    for (int u = 0; u < 2; ++u) x[u] = mfma32(kf[u], qf[k], x[u]);
+                    if constexpr (kLo) {
+                        const f16x8 ql = *reinterpret_cast<const f16x8 *>(qlo + k * 1024);
 #pragma unroll
-                            for (int p = 0; p < NP; ++p) x = mfma32(kf, qf[p][k], x);
-                        }
+                        for (int u = 0; u < 2; ++u) x[u] = mfma32(kf[u], ql, x[u]);
+                    }
+                }
+            };
+            if constexpr (kPost) {
+                const float *ks = reinterpret_cast<const float *>(buf + kKBytes + kVBytes) + 8 * hh;
+#pragma unroll
+                for (int q = 0; q < NG; ++q) {
+                    f32x16 x[2] = {f32x16{}, f32x16{}};
+                    products(x, 4 * q, 4 * q + 4);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
 #pragma unroll
                         for (int i = 0; i < 16; i += 4) {
-                            const float4 f = *reinterpret_cast<const float4 *>(ks + q * kTile + (i >> 3) * 16 + (i & 7));
+                            const float4 f = *reinterpret_cast<const float4 *>(ks + q * kTile + 32 * u + (i >> 3) * 16 + (i & 7));
                             const float ff[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
                             for (int y = 0; y < 4; ++y)
-                                s[u][i + y] = q == 0 ? x[i + y] * ff[y] : fmaf(x[i + y], ff[y], s[u][i + y]);
+                                s[u][i + y] = q == 0 ? x[u][i + y] * ff[y] : fmaf(x[u][i + y], ff[y], s[u][i + y]);
                         }
-                    }
-                } else {
-                    s[u] = f32x16{};
-#pragma unroll
-                    for (int k = 0; k < NK; ++k) {
-                        const f16x8 kf = *reinterpret_cast<const f16x8 *>(buf + (2 * k + hh) * kKStride + (32 * u + mtok) * 16);
-#pragma unroll
-                        for (int p = 0; p < NP; ++p) s[u] = mfma32(kf, qf[p][k], s[u]);
-                    }
                 }
+            } else {
+                s[0] = s[1] = f32x16{};
+                products(s, 0, NK);
             }
             // scores in units of smul (log2 e times the scale's factors), or, where the
             // terms are not linear, in log2 units already
@@ -435,11 +475,17 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
                 unit = 1.f;
             }
             if (a.slopes) {
+                const bool slots = a.tree && t0 + kTile > base;
+                const float far = (float)(col.pos - t0 - 8 * hh);
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        s[u][i] = s[u][i] * unit - col.slope * col.distance(a, t0 + 32 * u + (i >> 3) * 16 + 8 * hh + (i & 7), s0, n, base);
+                    for (int i = 0; i < 16; ++i) {
+                        const int t = 32 * u + (i >> 3) * 16 + (i & 7);
+                        float dist = fabsf(far - (float)t);
+                        if (slots) dist = col.distance(a, t0 + 8 * hh + t, s0, n, base);
+                        s[u][i] = fmaf(s[u][i], unit, -col.slope * dist);
+                    }
                 unit = 1.f;
             }
             const bool full = p0 >= 0 && p1 >= 0 && t0 >= reach.lo_all && t0 + kTile <= reach.hi_all;
@@ -547,7 +593,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
 
 template <int D, int BITS, bool ROT>
 static hipError_t wide_launch(const CacheAttnArgs &a, hipStream_t s) {
-    constexpr int NW = 4;
+    constexpr int NW = 8;
     const int64_t ctiles = ((int64_t)a.max_q * a.G + 32 * NW - 1) / (32 * NW);
     const int64_t grid = a.splits * ctiles * a.c.H * a.c.batch;
     if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
