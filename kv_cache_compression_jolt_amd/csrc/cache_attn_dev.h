@@ -9,6 +9,38 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 
+// Which (sequence, KV head, columns, token range) a workgroup has.  Workgroups
+// go to the 8 XCDs in turn; all of one (sequence, head) stay on one XCD, whose L2
+// then serves its rows of the cache, and the units are dealt out one by one, so
+// that sequences of unequal length spread over all XCDs.  Fewer than 32 units
+// that 8 does not divide are left in plain order (some XCDs would stay idle).
+struct AttnTile {
+    int b, h, ct, split;
+    bool valid;
+};
+__host__ __device__ __forceinline__ bool attn_by_xcd(int64_t units) { return units % 8 == 0 || units >= 32; }
+__host__ __device__ __forceinline__ int64_t attn_grid(int64_t units, int64_t per) {
+    return (attn_by_xcd(units) ? (units + 7) / 8 * 8 : units) * per;
+}
+__device__ __forceinline__ AttnTile attn_tile(const CacheAttnArgs &a, int ctiles) {
+    const uint32_t units = (uint32_t)a.c.batch * a.c.H, per = (uint32_t)ctiles * a.splits, w = blockIdx.x;
+    uint32_t u, in;
+    if (attn_by_xcd(units)) {
+        u = w / 8 / per * 8 + w % 8;
+        in = w / 8 % per;
+    } else {
+        u = w / per;
+        in = w % per;
+    }
+    AttnTile t;
+    t.valid = u < units;
+    t.b = u / a.c.H;
+    t.h = u % a.c.H;
+    t.ct = ctiles - 1 - in / a.splits;                 // later rows see more: they start first
+    t.split = in % a.splits;
+    return t;
+}
+
 // bits e = 0..7 set where lo <= tb + e < hi (all three in 0 .. 2^30 or, for lo, above)
 __device__ __forceinline__ uint32_t range8(int tb, int lo, int hi) {
     const int h = min(max(hi - tb, 0), 8), l = min(max(lo - tb, 0), 8);
@@ -93,6 +125,14 @@ struct Reach {
         if (a.tree) hi_any = len;
         hi_any = min(max(hi_any, prefix), len);
         hi_all = min(hi_all, len);
+    }
+    // the same in every lane: into scalar registers
+    __device__ __forceinline__ void uniform() {
+        lo_any = __builtin_amdgcn_readfirstlane(lo_any);
+        hi_any = __builtin_amdgcn_readfirstlane(hi_any);
+        lo_all = __builtin_amdgcn_readfirstlane(lo_all);
+        hi_all = __builtin_amdgcn_readfirstlane(hi_all);
+        first_any = __builtin_amdgcn_readfirstlane(first_any);
     }
     // the first token any column may see, the prefix included
     __device__ __forceinline__ int begin(int prefix) const {

@@ -122,12 +122,9 @@ __device__ __forceinline__ constexpr int value_feature(int i, int m) {
 template <int D, int BITS, bool ROT>
 __global__ __launch_bounds__(64 * kWaves) void k_cache_attn(CacheAttnArgs a, int ctiles) {
     constexpr int NK = D / 32, NV = D / 16, NG = D / 64, KU = BITS / 4;
-    int64_t w = blockIdx.x;
-    const int split = (int)(w % a.splits);
-    w /= a.splits;
-    const int ct = (int)(w % ctiles);
-    w /= ctiles;
-    const int h = (int)(w % a.c.H), b = (int)(w / a.c.H);
+    const AttnTile id = attn_tile(a, ctiles);
+    if (!id.valid) return;
+    const int b = id.b, h = id.h, ct = id.ct, split = id.split;
     int s0;
     const int nall = ragged_rows(a.starts, b, a.total, &s0), n = min(nall, a.max_q);
     if (ct * kCols >= n * a.G) return;
@@ -450,7 +447,7 @@ __global__ __launch_bounds__(256) void k_cache_attn_join(CacheAttnArgs a) {
 template <int D, int BITS, bool ROT>
 static hipError_t attn_launch(const CacheAttnArgs &a, hipStream_t s) {
     const int ctiles = (int)(((int64_t)a.max_q * a.G + kCols - 1) / kCols);
-    const int64_t grid = (int64_t)a.splits * ctiles * a.c.H * a.c.batch;
+    const int64_t grid = attn_grid((int64_t)a.c.batch * a.c.H, (int64_t)a.splits * ctiles);
     if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
     KTimeScope kts("k_cache_attn", s);
     hipLaunchKernelGGL((k_cache_attn<D, BITS, ROT>), dim3((unsigned)grid), dim3(64 * kWaves), 0, s, a, ctiles);

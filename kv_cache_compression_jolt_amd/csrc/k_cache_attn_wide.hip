@@ -28,6 +28,8 @@ namespace {
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kTile = 64;                              // tokens of a tile
 
@@ -101,25 +103,22 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
     constexpr int kKStride = kTile * 16 + 32;          // bytes of a K chunk (8 features of 64 tokens), padded
     constexpr int kKBytes = D / 8 * kKStride, kVBytes = kTile / 8 * D * 16;
     constexpr int kSBytes = kPost ? NG * kTile * 4 : 0;
-    constexpr int kBuf = kKBytes + kVBytes + kSBytes;
+    constexpr int kVBuf = kVBytes + kSBytes;           // the K scales of 8-bit codes lie behind V
     constexpr int kOutCols = 16;                       // columns of a wave that leave through LDS together
     constexpr int kOut = NW * kOutCols * (D + 4) * 4;
-    constexpr int kMain = 2 * kBuf > kOut ? 2 * kBuf : kOut;
+    constexpr int kMain = 2 * kKBytes + 3 * kVBuf > kOut ? 2 * kKBytes + 3 * kVBuf : kOut;
     constexpr bool kLo = ROT;                          // the queries' second parts stay in LDS: a lane's own fragments
     __shared__ __align__(16) uint8_t lds[kMain + (kLo ? NW * NK * 1024 : 0)];
     uint8_t *const qlo = lds + kMain + (threadIdx.x >> 6) * (NK * 1024) + (threadIdx.x & 63) * 16;
     __shared__ int reach_all[NW][3];
+    // what the columns see, read back only for tiles that need masks or distances
+    __shared__ __align__(16) uint8_t cols[NW * 32 * sizeof(Column)];
     typedef TileRegs<D, BITS, NT> Regs;
     constexpr int UPT = Regs::UPT, KU = Regs::kU, FS = Regs::FS;
 
-    // contiguous ranges of (sequence, head, columns, split) to an XCD: tiles of one head share its L2
-    int64_t w = blockIdx.x;
-    if (gridDim.x % 8 == 0) w = (w % 8) * (gridDim.x / 8) + w / 8;
-    const int split = (int)(w % a.splits);
-    w /= a.splits;
-    const int ct = ctiles - 1 - (int)(w % ctiles);     // later rows see more: they start first
-    w /= ctiles;
-    const int h = (int)(w % a.c.H), b = (int)(w / a.c.H);
+    const AttnTile id = attn_tile(a, ctiles);
+    if (!id.valid) return;
+    const int b = id.b, h = id.h, ct = id.ct, split = id.split;
     int s0;
     const int nall = ragged_rows(a.starts, b, a.total, &s0), n = min(nall, a.max_q), ncol = n * a.G;
     if (ct * 32 * NW >= ncol) return;
@@ -198,10 +197,13 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
     // ---- what the wave's columns see, and the workgroup's range of tiles
     const int c = c0 + m;
     const bool cv = c < ncol;
-    const Column col(a, s0, n, base, len, prefix, h, c, cv);
-    Reach reach(col, cv);
+    const Column mine(a, s0, n, base, len, prefix, h, c, cv);
+    if (hh == 0) reinterpret_cast<Column *>(cols)[32 * wave + m] = mine;
+    auto column = [&]() -> const Column & { return reinterpret_cast<const Column *>(cols)[32 * wave + m]; };
+    Reach reach(mine, cv);
     reach.join<32>();
     reach.clip(a, len, prefix);
+    reach.uniform();
     if (lane == 0) {
         reach_all[wave][0] = active ? reach.begin(prefix) : 0x7FFFFFFF;
         reach_all[wave][1] = active ? reach.hi_any : 0;
@@ -215,6 +217,9 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
         end = max(end, reach_all[x][1]);
         lo_any = min(lo_any, reach_all[x][2]);
     }
+    begin = __builtin_amdgcn_readfirstlane(begin);
+    end = __builtin_amdgcn_readfirstlane(end);
+    lo_any = __builtin_amdgcn_readfirstlane(lo_any);
     const int tile0 = begin / kTile, ntile = end > begin ? (end + kTile - 1) / kTile - tile0 : 0;
     const int per = (ntile + a.splits - 1) / a.splits;
     const int ts = tile0 + split * per, te = min(ts + per, tile0 + ntile);
@@ -226,16 +231,23 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
     for (int i = 0; i < NF; ++i) acc[i] = f32x16{};
     float mrun = neg_inf(), lrun = 0.f;
     int erun = kTop;                                   // exponent field of acc's unit: the largest V scale so far
-    const float mul = a.scale * kLog2e * qmul, cap_in = a.cap > 0.f ? a.scale / a.cap * (2.f * kLog2e) * qmul : 0.f;
+    const float mul = a.scale * kLog2e * qmul;
+    const bool capped = a.cap > 0.f, sloped = a.slopes != nullptr, tree = a.tree != nullptr;
 
     // tiles between a prefix and the window are skipped by the whole workgroup
     auto next_tile = [&](int t) {
         const int skip_to = lo_any / kTile;
         return t * kTile >= prefix && t < skip_to ? skip_to : t;
     };
-    auto page_of = [&](int t, int half) -> int {
-        return t < te ? cache_page(a.c, b, t * kTile + 32 * half) : -1;
+    // Pages of the tiles' halves, 32 tiles' worth in a register (lane 2 i + half:
+    // tile seen + i) and loaded anew when a tile lies past them, so that the tile
+    // loop holds no scalar load (it would drain with the LDS reads).
+    int seen = ts, pages;
+    auto load_pages = [&]() {
+        const int tok = (seen + (lane >> 1)) * kTile + 32 * (lane & 1);
+        pages = tok < len && seen + (lane >> 1) < te ? cache_page(a.c, b, tok) : -1;
     };
+    auto page_of = [&](int t, int half) -> int { return __builtin_amdgcn_readlane(pages, 2 * (t - seen) + half); };
     // units of K: consecutive ones of a row; units of V: features f, f + FS, .. of
     // a block of 8 tokens.  The first half of the waves has the tile's first 32
     // tokens, so that a wave reads one page.
@@ -245,57 +257,53 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
     const uint32_t koff = (ktok & 31) * (D * BITS / 8) + ku0 * (4 * KU), voff = (vblk & 3) * (D * BITS) + vf * (4 * KU);
     const uint32_t all_off = (uint32_t)(hh ? pl.v_scales : pl.k_scales) + ((NG == 2 ? m >> 4 : 0) * P + 2 * (m & 15)) * 2;
     Regs rg;
+    // The loads go through buffer descriptors of the two page blocks: a uniform
+    // base, a uniform offset and one 32-bit offset a lane, bounded by the block.
+    auto block = [&](int page) {
+        // a half without a page reads page 0 (never used: its scales count as 0)
+        const uint8_t *p = a.c.pool + (page >= 0 ? cache_block_offset(a.c, page, h) : 0);
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), 0, (int)pl.bytes, 0x00027000);
+    };
     auto fetch = [&](int t, int p0, int p1) {
-        const int t0 = t * kTile;
-        // a half without a page reads page 0 (never used: its scales count as 0); a
-        // call with pages == 0 has no valid page and fetches nothing
-        const uint8_t *b0 = a.c.pool + (p0 >= 0 ? cache_block_offset(a.c, p0, h) : 0);
-        const uint8_t *b1 = a.c.pool + (p1 >= 0 ? cache_block_offset(a.c, p1, h) : 0);
-        const int i0 = t0 & (P - 1), i1 = (t0 + 32) & (P - 1);
-        const uint8_t *bw = second ? b1 : b0;
-        const int iw = second ? i1 : i0;
-        {
-            const uint8_t *p = bw + iw * (D * BITS / 8) + koff;
-            constexpr int N = UPT * KU;
-            if constexpr (N == 1) rg.k[0] = *reinterpret_cast<const uint32_t *>(p);
-            else if constexpr (N == 2) {
-                const uint2 v = *reinterpret_cast<const uint2 *>(p);
-                rg.k[0] = v.x; rg.k[1] = v.y;
-            } else {
+        const int t0 = t * kTile, i0 = t0 & (P - 1), i1 = (t0 + 32) & (P - 1), iw = second ? i1 : i0;
+        const auto bw = block(second ? p1 : p0);
+        constexpr int N = UPT * KU;
+        if constexpr (N == 1) rg.k[0] = __builtin_amdgcn_raw_buffer_load_b32(bw, koff, iw * (D * BITS / 8), 0);
+        else if constexpr (N == 2) {
+            const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(bw, koff, iw * (D * BITS / 8), 0);
+            rg.k[0] = v.x; rg.k[1] = v.y;
+        } else {
 #pragma unroll
-                for (int i = 0; i < N; i += 4) {
-                    const uint4 v = *reinterpret_cast<const uint4 *>(p + 4 * i);
-                    rg.k[i] = v.x; rg.k[i + 1] = v.y; rg.k[i + 2] = v.z; rg.k[i + 3] = v.w;
-                }
-            }
-#pragma unroll
-            for (int q = 0; q < NG; ++q)
-                rg.ks[q] = *reinterpret_cast<const uint16_t *>(bw + pl.k_scales + (q * P + iw) * 2 + (uint32_t)(ktok & 31) * 2u);
-        }
-        {
-            const uint8_t *p = bw + pl.v_codes + (iw >> 3) * (D * BITS) + voff;
-#pragma unroll
-            for (int x = 0; x < UPT; ++x) {
-                if constexpr (KU == 1) rg.v[x] = *reinterpret_cast<const uint32_t *>(p + FS * x * 4);
-                else {
-                    const uint2 v = *reinterpret_cast<const uint2 *>(p + FS * x * 8);
-                    rg.v[2 * x] = v.x; rg.v[2 * x + 1] = v.y;
-                }
-            }
-#pragma unroll
-            for (int q = 0; q < NG; ++q) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(bw + pl.v_scales + (q * P + iw) * 2 + (uint32_t)(vblk & 3) * 16u);
-                rg.vs[q][0] = v.x; rg.vs[q][1] = v.y; rg.vs[q][2] = v.z; rg.vs[q][3] = v.w;
+            for (int i = 0; i < N; i += 4) {
+                const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(bw, koff + 4 * i, iw * (D * BITS / 8), 0);
+                rg.k[i] = v.x; rg.k[i + 1] = v.y; rg.k[i + 2] = v.z; rg.k[i + 3] = v.w;
             }
         }
-        rg.all[0] = *reinterpret_cast<const uint32_t *>(b0 + i0 * 2 + all_off);
-        rg.all[1] = *reinterpret_cast<const uint32_t *>(b1 + i1 * 2 + all_off);
+#pragma unroll
+        for (int q = 0; q < NG; ++q)
+            rg.ks[q] = __builtin_amdgcn_raw_buffer_load_b16(bw, (ktok & 31) * 2, (int)pl.k_scales + (q * P + iw) * 2, 0);
+#pragma unroll
+        for (int x = 0; x < UPT; ++x) {
+            const int so = (int)pl.v_codes + (iw >> 3) * (D * BITS);
+            if constexpr (KU == 1) rg.v[x] = __builtin_amdgcn_raw_buffer_load_b32(bw, voff + FS * x * 4, so, 0);
+            else {
+                const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(bw, voff + FS * x * 8, so, 0);
+                rg.v[2 * x] = v.x; rg.v[2 * x + 1] = v.y;
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < NG; ++q) {
+            const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(bw, (vblk & 3) * 16, (int)pl.v_scales + (q * P + iw) * 2, 0);
+            rg.vs[q][0] = v.x; rg.vs[q][1] = v.y; rg.vs[q][2] = v.z; rg.vs[q][3] = v.w;
+        }
+        rg.all[0] = __builtin_amdgcn_raw_buffer_load_b32(block(p0), all_off, i0 * 2, 0);
+        rg.all[1] = __builtin_amdgcn_raw_buffer_load_b32(block(p1), all_off, i1 * 2, 0);
     };
     // registers -> LDS; returns the exponent field of the tile's K unit, and raises enext
     int enext = kTop;                                  // (the floor keeps a zero scale zero)
     uint32_t magic = 0x64006400u;
     asm("" : "+v"(magic));
-    auto stage = [&](int t, int p0, int p1, uint8_t *buf) -> int {
+    auto stage = [&](int t, int p0, int p1, uint8_t *kbuf, uint8_t *vbuf) -> int {
         const int t0 = t * kTile;
         const int lim0 = p0 >= 0 ? len : 0, lim1 = p1 >= 0 ? len : 0;      // tokens below these count, by half
         const bool whole = t0 + kTile <= min(lim0, lim1);
@@ -363,14 +371,14 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
 #pragma unroll
                 for (int i = 0; i < 4; ++i) y[i] *= sc;
             }
-            *reinterpret_cast<uint4 *>(buf + (4 * kk + g) * kKStride + ktok * 16) =
+            *reinterpret_cast<uint4 *>(kbuf + (4 * kk + g) * kKStride + ktok * 16) =
                 make_uint4(u32(y[0]), u32(y[1]), u32(y[2]), u32(y[3]));
         }
         if constexpr (kPost) {
             if (ku0 == 0)
 #pragma unroll
                 for (int q = 0; q < NG; ++q)
-                    reinterpret_cast<float *>(buf + kKBytes + kVBytes)[q * kTile + ktok] =
+                    reinterpret_cast<float *>(vbuf + kVBytes)[q * kTile + ktok] =
                         kbad ? __builtin_nanf("") : bf16_to_f32(rg.ks[q]);
         }
         f16x2 sc[NG][4];
@@ -385,7 +393,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
             const int q = NG == 1 ? 0 : (FS * x) / 64;
 #pragma unroll
             for (int i = 0; i < 4; ++i) y[i] *= sc[q][i];
-            *reinterpret_cast<uint4 *>(buf + kKBytes + (vblk * D + vf + FS * x) * 16) =
+            *reinterpret_cast<uint4 *>(vbuf + (vblk * D + vf + FS * x) * 16) =
                 make_uint4(u32(y[0]), u32(y[1]), u32(y[2]), u32(y[3]));
         }
         return ek;
@@ -393,118 +401,191 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
 
     // token of K row m: bits 2 and 3 exchanged, so that a lane's scores are 8 consecutive tokens twice
     const int mtok = (m & 19) | ((m & 4) << 1) | ((m & 8) >> 1);
-    int tile = next_tile(ts);
-    int p0 = page_of(tile, 0), p1 = page_of(tile, 1);
-    int ek = 0, cur = 0;
-    __syncthreads();                                   // the queries have left LDS
-    if (tile < te) {
-        if (p0 >= 0 || p1 >= 0) {
-            fetch(tile, p0, p1);
-            ek = stage(tile, p0, p1, lds);
+    uint8_t *const vlds = lds + 2 * kKBytes;
+
+    // Two groups of waves, one on each half of every SIMD's slots, take turns at
+    // the matrix cores: while one multiplies (weights of its last tile times V,
+    // then queries times the K of the next), the other runs softmax and staging
+    // on the vector unit; a barrier ends each turn.
+    //   turn    2 i - 2        2 i - 1        2 i            2 i + 1
+    //   early   M(i-1)         V(i-1) st(i)   M(i)           V(i) st(i+1)
+    //   late    V(i-2) st(i)   M(i-1)         V(i-1) st(i+1) M(i)
+    // Both halves of tile i are staged before turn 2 i.  A turn that stages tile
+    // i overlaps products on K(i-1) and V(i-2): two K buffers, three V buffers.
+    const bool late = second;
+    struct Tile { int t, p0, p1, ek, ev; };
+    auto look = [&](int t) {
+        if (t >= te) return Tile{t, -1, -1, kTop, kTop};
+        if (t >= seen + 32) {
+            seen = t;
+            load_pages();
         }
-    }
-    __syncthreads();
-    while (tile < te) {
-        const int nt = next_tile(tile + 1);
-        const int n0 = page_of(nt, 0), n1 = page_of(nt, 1);
-        const bool more = n0 >= 0 || n1 >= 0;
-        if (more) fetch(nt, n0, n1);
-        const int t0 = tile * kTile;
-        const uint8_t *buf = lds + cur * kBuf;
-        const bool any = active && (p0 >= 0 || p1 >= 0) && t0 < reach.hi_any &&
-                         (t0 + kTile > reach.lo_any || t0 < prefix);
-        if (any) {
-            if (enext > erun) {                        // the V unit grew
-                const float f = __builtin_ldexpf(1.f, erun - enext);
+        return Tile{t, page_of(t, 0), page_of(t, 1), kTop, kTop};
+    };
+    // field by field: a choice between the structs themselves would put them in memory
+    auto of_group = [&](Tile e, Tile l) {
+        return Tile{late ? l.t : e.t, late ? l.p0 : e.p0, late ? l.p1 : e.p1, late ? l.ek : e.ek, late ? l.ev : e.ev};
+    };
+    auto stage_tile = [&](Tile &x, int nth) {
+        x.ek = stage(x.t, x.p0, x.p1, lds + (nth & 1) * kKBytes, vlds + (nth % 3) * kVBuf);
+        x.ev = enext;
+    };
+    f32x16 s[2];
+    f16x8 pf[4];
+    // In both products the next step's fragments are read from LDS before the
+    // present step's products are issued, in the order written here.
+    auto times_v = [&](int nth) {
+        const uint8_t *vb = vlds + (nth % 3) * kVBuf;
+        constexpr int A = 5;                           // pairs of fragments held: four ahead of the one in use
+        f16x8 f[A][2];
+        auto read = [&](int g) {                       // pair g: block of tokens g / (NF/2), features of 2 (g % (NF/2))
 #pragma unroll
-                for (int i = 0; i < NF; ++i) acc[i] *= f;
-                erun = enext;
+            for (int i = 0; i < 2; ++i)
+                f[g % A][i] = *reinterpret_cast<const f16x8 *>(
+                    vb + ((2 * (g / (NF / 2)) + hh) * D + 32 * (2 * (g % (NF / 2)) + i) + m) * 16);
+        };
+        constexpr int N = 4 * NF / 2;
+#pragma unroll
+        for (int g = 0; g < A - 1; ++g) read(g);
+#pragma unroll
+        for (int g = 0; g < N; ++g) {
+            if (g + A - 1 < N) read(g + A - 1);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int x = 2 * (g % (NF / 2)) + i;
+                acc[x] = mfma32(f[g % A][i], pf[g / (NF / 2)], acc[x]);
             }
-            const float kunit = kPost ? 1.f : __builtin_ldexpf(1.f, ek - 127 - (kTop - 15));   // 2^E
-            const float smul = mul * kunit, scap = cap_in * kunit;
-            f32x16 s[2];
-            // s[u] += K rows of half u times the queries, features 16 k0 .. 16 (k1) - 1
-            auto products = [&](f32x16 (&x)[2], int k0, int k1) {
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    auto times_k = [&](int nth) {
+        const uint8_t *kb = lds + (nth & 1) * kKBytes;
+        // x[u] += K rows of half u times the queries, features 16 k0 .. 16 k1 - 1
+        auto products = [&](f32x16 (&x)[2], int k0, int k1) {
+            constexpr int A = kPost ? 2 : 3;           // steps held: the ones ahead of the one in use
+            f16x8 kf[A][2], ql[A];
+            auto read = [&](int k) {
 #pragma unroll
-                for (int k = k0; k < k1; ++k) {
-                    f16x8 kf[2];
-#pragma unroll
-                    for (int u = 0; u < 2; ++u)
-                        kf[u] = *reinterpret_cast<const f16x8 *>(buf + (2 * k + hh) * kKStride + (32 * u + mtok) * 16);
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) x[u] = mfma32(kf[u], qf[k], x[u]);
-                    if constexpr (kLo) {
-                        const f16x8 ql = *reinterpret_cast<const f16x8 *>(qlo + k * 1024);
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) x[u] = mfma32(kf[u], ql, x[u]);
-                    }
-                }
+                for (int u = 0; u < 2; ++u)
+                    kf[k % A][u] = *reinterpret_cast<const f16x8 *>(kb + (2 * k + hh) * kKStride + (32 * u + mtok) * 16);
+                if constexpr (kLo) ql[k % A] = *reinterpret_cast<const f16x8 *>(qlo + k * 1024);
             };
-            if constexpr (kPost) {
-                const float *ks = reinterpret_cast<const float *>(buf + kKBytes + kVBytes) + 8 * hh;
 #pragma unroll
-                for (int q = 0; q < NG; ++q) {
-                    f32x16 x[2] = {f32x16{}, f32x16{}};
-                    products(x, 4 * q, 4 * q + 4);
+            for (int k = k0; k < k0 + A - 1; ++k) read(k);
 #pragma unroll
-                    for (int u = 0; u < 2; ++u)
+            for (int k = k0; k < k1; ++k) {
+                if (k + A - 1 < k1) read(k + A - 1);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                        for (int i = 0; i < 16; i += 4) {
-                            const float4 f = *reinterpret_cast<const float4 *>(ks + q * kTile + 32 * u + (i >> 3) * 16 + (i & 7));
-                            const float ff[4] = {f.x, f.y, f.z, f.w};
+                for (int u = 0; u < 2; ++u) x[u] = mfma32(kf[k % A][u], qf[k], x[u]);
+                if constexpr (kLo)
 #pragma unroll
-                            for (int y = 0; y < 4; ++y)
-                                s[u][i + y] = q == 0 ? x[u][i + y] * ff[y] : fmaf(x[u][i + y], ff[y], s[u][i + y]);
-                        }
-                }
-            } else {
-                s[0] = s[1] = f32x16{};
-                products(s, 0, NK);
+                    for (int u = 0; u < 2; ++u) x[u] = mfma32(kf[k % A][u], ql[k % A], x[u]);
+                __builtin_amdgcn_sched_barrier(0);
             }
-            // scores in units of smul (log2 e times the scale's factors), or, where the
-            // terms are not linear, in log2 units already
-            float unit = smul;
-            if (a.cap > 0.f) {
+        };
+        if constexpr (kPost) {
+            const float *ks = reinterpret_cast<const float *>(vlds + (nth % 3) * kVBuf + kVBytes) + 8 * hh;
+#pragma unroll
+            for (int q = 0; q < NG; ++q) {
+                f32x16 x[2] = {f32x16{}, f32x16{}};
+                products(x, 4 * q, 4 * q + 4);
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float x = __builtin_amdgcn_exp2f(-fabsf(s[u][i] * scap));
-                        s[u][i] = copysignf((1.f - x) * __builtin_amdgcn_rcpf(1.f + x), s[u][i]) * (a.cap * kLog2e);
+                    for (int e = 0; e < 16; e += 4) {
+                        const float4 f = *reinterpret_cast<const float4 *>(ks + q * kTile + 32 * u + (e >> 3) * 16 + (e & 7));
+                        const float ff[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            s[u][e + y] = q == 0 ? x[u][e + y] * ff[y] : fmaf(x[u][e + y], ff[y], s[u][e + y]);
+                    }
+            }
+        } else {
+            s[0] = s[1] = f32x16{};
+            products(s, 0, NK);
+        }
+    };
+
+    const int first_tile = next_tile(ts);
+    if (a.c.pages > 0 && first_tile < te) {            // (no page: nothing to see)
+        seen = first_tile;
+        load_pages();
+        Tile cur = look(first_tile), nxt = look(next_tile(first_tile + 1));
+        fetch(cur.t, cur.p0, cur.p1);
+        stage_tile(cur, 0);
+        if (late) {
+            fetch(nxt.t, nxt.p0, nxt.p1);
+            stage_tile(nxt, 1);
+        }
+        Tile nx2 = look(next_tile(nxt.t + 1));
+        __syncthreads();
+        if (late) __syncthreads();                     // the late group's first turn: early multiplies
+        {
+            const Tile f = of_group(nxt, nx2);
+            fetch(f.t, f.p0, f.p1);
+        }
+        times_k(0);
+        __syncthreads();
+        for (int i = 0;; ++i) {
+            const int t0 = cur.t * kTile;
+            const Tile nx3 = look(next_tile(nx2.t + 1));
+            // ---- V: softmax of this tile, staging of a later one
+            if (cur.ev > erun) {                   // the V unit grew
+                const float f = __builtin_ldexpf(1.f, erun - cur.ev);
+#pragma unroll
+                for (int x = 0; x < NF; ++x) acc[x] *= f;
+                erun = cur.ev;
+            }
+            const float kunit = kPost ? 1.f : __builtin_ldexpf(1.f, cur.ek - 127 - (kTop - 15));   // 2^E
+            // scores in units of smul (log2 e times the scale's factors), or, where
+            // the terms are not linear, in log2 units already
+            float unit = mul * kunit;
+            if (capped) {
+                const float scap = unit * (2.f / a.cap);
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float x = __builtin_amdgcn_exp2f(-fabsf(s[u][e] * scap));
+                        s[u][e] = copysignf((1.f - x) * __builtin_amdgcn_rcpf(1.f + x), s[u][e]) * (a.cap * kLog2e);
                     }
                 unit = 1.f;
             }
-            if (a.slopes) {
-                const bool slots = a.tree && t0 + kTile > base;
+            if (sloped) {
+                const Column col = column();
+                const bool slots = tree && t0 + kTile > base;
                 const float far = (float)(col.pos - t0 - 8 * hh);
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int t = 32 * u + (i >> 3) * 16 + (i & 7);
+                    for (int e = 0; e < 16; ++e) {
+                        const int t = 32 * u + (e >> 3) * 16 + (e & 7);
                         float dist = fabsf(far - (float)t);
                         if (slots) dist = col.distance(a, t0 + 8 * hh + t, s0, n, base);
-                        s[u][i] = fmaf(s[u][i], unit, -col.slope * dist);
+                        s[u][e] = fmaf(s[u][e], unit, -col.slope * dist);
                     }
                 unit = 1.f;
             }
-            const bool full = p0 >= 0 && p1 >= 0 && t0 >= reach.lo_all && t0 + kTile <= reach.hi_all;
+            const bool full = cur.p0 >= 0 && cur.p1 >= 0 && t0 >= reach.lo_all && t0 + kTile <= reach.hi_all;
             if (!full) {
+                const Column col = column();
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        uint32_t vis = col.sees8(a.tree != nullptr, base, t0 + 32 * u + 16 * x + 8 * hh);
-                        if ((u ? p1 : p0) < 0) vis = 0;
+                        uint32_t vis = col.sees8(tree, base, t0 + 32 * u + 16 * x + 8 * hh);
+                        if ((u ? cur.p1 : cur.p0) < 0) vis = 0;
 #pragma unroll
                         for (int e = 0; e < 8; ++e) s[u][8 * x + e] = (vis >> e) & 1 ? s[u][8 * x + e] : neg_inf();
                     }
             }
             float mx = s[0][0];
 #pragma unroll
-            for (int i = 1; i < 16; ++i) mx = fmaxf(mx, s[0][i]);
+            for (int e = 1; e < 16; ++e) mx = fmaxf(mx, s[0][e]);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[1][i]);
+            for (int e = 0; e < 16; ++e) mx = fmaxf(mx, s[1][e]);
             mx *= unit;
             if (__any(mx > mrun + 8.f)) {
                 mx = fmaxf(fmaxf(mx, __shfl_xor(mx, 32)), mrun);
@@ -512,36 +593,45 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
                 mrun = mx;
                 lrun *= alpha;
 #pragma unroll
-                for (int i = 0; i < NF; ++i) acc[i] *= alpha;
+                for (int x = 0; x < NF; ++x) acc[x] *= alpha;
             }
             const float mu = mrun == neg_inf() ? 0.f : -mrun;
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int x = 0; x < 4; ++x) {
+                float p[8];
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    float p[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        p[e] = __builtin_amdgcn_exp2f(fmaf(s[u][8 * x + e], unit, mu));
-                        lrun += p[e];
-                    }
-                    const f16x8 pf = __builtin_bit_cast(f16x8, make_uint4(f16_pair(p[0], p[1]), f16_pair(p[2], p[3]),
-                                                                          f16_pair(p[4], p[5]), f16_pair(p[6], p[7])));
-#pragma unroll
-                    for (int i = 0; i < NF; ++i) {
-                        const f16x8 vf8 = *reinterpret_cast<const f16x8 *>(
-                            buf + kKBytes + ((4 * u + 2 * x + hh) * D + 32 * i + m) * 16);
-                        acc[i] = mfma32(vf8, pf, acc[i]);
-                    }
+                for (int e = 0; e < 8; ++e) {
+                    p[e] = __builtin_amdgcn_exp2f(fmaf(s[x >> 1][8 * (x & 1) + e], unit, mu));
+                    lrun += p[e];
                 }
+                pf[x] = __builtin_bit_cast(f16x8, make_uint4(f16_pair(p[0], p[1]), f16_pair(p[2], p[3]),
+                                                             f16_pair(p[4], p[5]), f16_pair(p[6], p[7])));
+                asm volatile("" : "+v"(pf[x]), "+v"(lrun));   // computed in this turn, not sunk into the next
+            }
+            Tile st = of_group(nxt, nx2);
+            stage_tile(st, late ? i + 2 : i + 1);
+            nxt.ek = late ? nxt.ek : st.ek;
+            nxt.ev = late ? nxt.ev : st.ev;
+            nx2.ek = late ? st.ek : nx2.ek;
+            nx2.ev = late ? st.ev : nx2.ev;
+            __syncthreads();
+            // ---- M: products
+            const bool last = nxt.t >= te;
+            if (!last) {
+                const Tile f = of_group(nx2, nx3);
+                fetch(f.t, f.p0, f.p1);
+            }
+            times_v(i);
+            if (last) break;
+            times_k(i + 1);
+            __syncthreads();
+            cur = nxt;
+            nxt = nx2;
+            nx2 = nx3;
         }
-        if (more) ek = stage(nt, n0, n1, lds + (cur ^ 1) * kBuf);
-        __syncthreads();
-        cur ^= 1;
-        tile = nt;
-        p0 = n0;
-        p1 = n1;
+        if (!late) __syncthreads();
     }
+    __syncthreads();
 
     // ---- rows out, 16 columns of the wave at a time
     if (!active) return;
@@ -595,7 +685,7 @@ template <int D, int BITS, bool ROT>
 static hipError_t wide_launch(const CacheAttnArgs &a, hipStream_t s) {
     constexpr int NW = 8;
     const int64_t ctiles = ((int64_t)a.max_q * a.G + 32 * NW - 1) / (32 * NW);
-    const int64_t grid = a.splits * ctiles * a.c.H * a.c.batch;
+    const int64_t grid = attn_grid((int64_t)a.c.batch * a.c.H, a.splits * ctiles);
     if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
     KTimeScope kts("k_cache_attn_wide", s);
     hipLaunchKernelGGL((k_cache_attn_wide<D, BITS, ROT, NW>), dim3((unsigned)grid), dim3(64 * NW), 0, s, a, (int)ctiles);
