@@ -73,6 +73,8 @@ struct AttnPlan {
 jolt_status cache_attn_check(const jolt_cache *c, int32_t batch, int32_t total, int32_t max_q, int32_t max_len,
                              int32_t q_heads, const char **msg);
 AttnPlan cache_attn_plan(const jolt_cache &c, int batch, int64_t total, int max_q, int max_len, int q_heads);
+// least tokens of a range, for a window and max_len
+int cache_attn_least(const AttnPlan &p, int max_q, int max_len, int window, bool prefix);
 int page_shift_of(int page_tokens);
 
 #if defined(__HIPCC__)
@@ -109,7 +111,7 @@ struct CacheAttnArgs {
     const float *merge_out, *merge_lse;
     float *ws_ml, *ws_part;
     float scale, cap;
-    int window, total, max_q, hq, G, splits;
+    int window, total, max_q, hq, G, splits, least;
 };
 hipError_t launch_cache_attention(const CacheAttnArgs &a, bool wide, int d, int bits, bool rotate, hipStream_t s);
 hipError_t launch_cache_attn_wide(const CacheAttnArgs &a, int d, int bits, bool rotate, hipStream_t s);

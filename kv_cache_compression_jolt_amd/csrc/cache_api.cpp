@@ -141,6 +141,7 @@ static jolt_status attn_call(jolt_handle h, const jolt_cache *cache, int32_t bat
     a.hq = q_heads;
     a.G = q_heads / cache->H;
     a.splits = p.splits;
+    a.least = cache_attn_least(p, max_q, max_len, terms->window, terms->prefix != nullptr);
     const hipError_t e = launch_cache_attention(a, p.wide, cache->d, cache->bits, cache->rotate != 0,
                                                 static_cast<hipStream_t>(stream));
     return e == hipSuccess ? JOLT_OK : hip_fail(h, e, "cache_attention");

@@ -74,16 +74,15 @@ jolt_status cache_attn_check(const jolt_cache *c, int32_t batch, int32_t total, 
 }
 
 // Query columns of a KV head and sequence: up to 32 go to the narrow kernel
-// (tiles of 16), more to the wide one (tiles of 128).  Token ranges: enough
-// workgroups for the 256 CUs (about four narrow or two wide ones each), none of
-// fewer than 256 (512) tokens.
+// (tiles of 16), more to the wide one (tiles of 256).  Token ranges: enough
+// workgroups for the 256 CUs, none of fewer than 256 (512) tokens.
 AttnPlan cache_attn_plan(const jolt_cache &c, int batch, int64_t total, int max_q, int max_len, int q_heads) {
     AttnPlan p{};
     const int64_t cols = (int64_t)max_q * (q_heads / c.H);
     p.wide = cols > 32;
-    const int64_t per = p.wide ? 256 : 16, want = p.wide ? 256 : 1024, least = p.wide ? 512 : 256;
+    const int64_t per = p.wide ? 256 : 16, want = p.wide ? 256 : 512, least = p.wide ? 512 : 256;
     const int64_t tiles = std::max<int64_t>(1, (int64_t)batch * c.H * ((cols + per - 1) / per));
-    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(max_len / least, want / tiles));
+    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(max_len / least, want / tiles), 256));
     if (p.splits > 1) {
         const size_t rows = (size_t)total * q_heads;
         p.ml_off = 0;
@@ -91,6 +90,15 @@ AttnPlan cache_attn_plan(const jolt_cache &c, int batch, int64_t total, int max_
         p.bytes = p.part_off + p.splits * rows * c.d * 4;
     }
     return p;
+}
+
+// A sequence shorter than the longest is cut into fewer ranges of the longest
+// one's size, not into as many small ones, so that a ragged batch's ranges take
+// equal time.
+int cache_attn_least(const AttnPlan &p, int max_q, int max_len, int window, bool prefix) {
+    int64_t seen = max_len;
+    if (window > 0 && !prefix) seen = std::min<int64_t>(seen, (int64_t)window + max_q);
+    return (int)((seen + p.splits - 1) / p.splits);
 }
 
 }  // namespace jolt

@@ -120,7 +120,7 @@ __device__ __forceinline__ constexpr int value_feature(int i, int m) {
 // fragments go from memory to registers, the next block's while this one is
 // computed) and join their sums through LDS at the end.
 template <int D, int BITS, bool ROT>
-__global__ __launch_bounds__(64 * kWaves) void k_cache_attn(CacheAttnArgs a, int ctiles) {
+__global__ __launch_bounds__(64 * kWaves, 2) void k_cache_attn(CacheAttnArgs a, int ctiles) {
     constexpr int NK = D / 32, NV = D / 16, NG = D / 64, KU = BITS / 4;
     const AttnTile id = attn_tile(a, ctiles);
     if (!id.valid) return;
@@ -128,12 +128,55 @@ __global__ __launch_bounds__(64 * kWaves) void k_cache_attn(CacheAttnArgs a, int
     int s0;
     const int nall = ragged_rows(a.starts, b, a.total, &s0), n = min(nall, a.max_q);
     if (ct * kCols >= n * a.G) return;
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, m = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, m = lane & 15, g = lane >> 4;
     const int len = cache_len(a.c, b), base = a.c.lens[b] - nall;
     const int prefix = a.prefix ? a.prefix[b] : 0;
 
     __shared__ __align__(16) float sm[kWaves * kCols * (D + 4)];
     __shared__ float sml[2][kWaves][kCols];
+
+    // ---- what the columns see
+    const int c = ct * kCols + m, ncol = n * a.G;
+    const bool cv = c < ncol;
+    const Column col(a, s0, n, base, len, prefix, h, c, cv);
+    Reach reach(col, cv);
+    reach.join<16>();
+    reach.clip(a, len, prefix);
+    reach.uniform();
+    const int lo_any = reach.lo_any, hi_any = reach.hi_any, lo_all = reach.lo_all, hi_all = reach.hi_all;
+    const int begin = reach.begin(prefix);
+
+    // ---- this workgroup's blocks
+    const int blk0 = begin >> 5, nblk = hi_any > begin ? ((hi_any + 31) >> 5) - blk0 : 0;
+    const int per = max((nblk + a.splits - 1) / a.splits, a.least >> 5);
+    const int bs = blk0 + split * per, be = min(bs + per, blk0 + nblk);
+
+    const int P = 1 << a.c.page_shift;
+    const PageLayout pl = page_layout(P, D, BITS);
+    // ---- this wave's blocks: bs + wave, then every kWaves-th.  The page numbers of
+    // its next 64 blocks sit in one register (lane i: block seen + i kWaves), and
+    // the first block's loads start before the queries are prepared.
+    int seen = bs + wave, pages = -1;
+    auto load_pages = [&]() {
+        const int blk = seen + lane * kWaves, t0 = blk << 5;
+        // blocks between a prefix and the window hold nothing visible
+        pages = blk < be && (t0 < prefix || t0 + 32 > lo_any) ? cache_page(a.c, b, t0) : -1;
+    };
+    auto page_of = [&](int blk) -> int {
+        if (blk >= be) return -1;
+        if (blk - seen >= 64 * kWaves) {
+            seen = blk;
+            load_pages();
+        }
+        return __builtin_amdgcn_readlane(pages, (blk - seen) / kWaves);
+    };
+    BlockRegs<D, BITS> even, odd;
+    auto load = [&](BlockRegs<D, BITS> &r, int blk, int page) {
+        if (page >= 0) r.load(a.c.pool + cache_block_offset(a.c, page, h), pl, P, (blk << 5) & (P - 1), m, g);
+    };
+    load_pages();
+    int page = page_of(bs + wave);
+    load(even, bs + wave, page);
 
     // ---- the queries in the cache's domain, one row per D / 8 lanes, through LDS
     {
@@ -201,23 +244,6 @@ __global__ __launch_bounds__(64 * kWaves) void k_cache_attn(CacheAttnArgs a, int
     }
     __syncthreads();                                    // sm is reused by the join
 
-    // ---- what the columns see
-    const int c = ct * kCols + m, ncol = n * a.G;
-    const bool cv = c < ncol;
-    const Column col(a, s0, n, base, len, prefix, h, c, cv);
-    Reach reach(col, cv);
-    reach.join<16>();
-    reach.clip(a, len, prefix);
-    const int lo_any = reach.lo_any, hi_any = reach.hi_any, lo_all = reach.lo_all, hi_all = reach.hi_all;
-    const int begin = reach.begin(prefix);
-
-    // ---- this workgroup's blocks, this wave's every kWaves-th
-    const int blk0 = begin >> 5, nblk = hi_any > begin ? ((hi_any + 31) >> 5) - blk0 : 0;
-    const int per = (nblk + a.splits - 1) / a.splits;
-    const int bs = blk0 + split * per, be = min(bs + per, blk0 + nblk);
-
-    const int P = 1 << a.c.page_shift;
-    const PageLayout pl = page_layout(P, D, BITS);
     f32x4 acc[NV], corr[NG];
 #pragma unroll
     for (int i = 0; i < NV; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -227,105 +253,99 @@ __global__ __launch_bounds__(64 * kWaves) void k_cache_attn(CacheAttnArgs a, int
     const float mul = a.scale * kLog2e, cap_mul = a.cap > 0.f ? a.scale / a.cap * (2.f * kLog2e) : 0.f;
     const bf16x8 ones = __builtin_bit_cast(bf16x8, make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u));
 
-    auto page_of = [&](int blk) -> int {                // -1: nothing to do there
-        if (blk >= be) return -1;
+    auto work = [&](const BlockRegs<D, BITS> &use, int blk) {
         const int t0 = blk << 5;
-        if (t0 >= prefix && t0 + 32 <= lo_any) return -1;
-        return cache_page(a.c, b, t0);
-    };
-    BlockRegs<D, BITS> cur, nxt;
-    int blk = bs + wave, page = page_of(blk);
-    if (page >= 0) cur.load(a.c.pool + cache_block_offset(a.c, page, h), pl, P, (blk << 5) & (P - 1), m, g);
-    for (; blk < be; blk += kWaves) {
-        const int pnext = page_of(blk + kWaves);
-        if (pnext >= 0)
-            nxt.load(a.c.pool + cache_block_offset(a.c, pnext, h), pl, P, ((blk + kWaves) << 5) & (P - 1), m, g);
-        if (page >= 0) {
-            const int t0 = blk << 5;
-            // scores: lane (column m) has tokens t0 + 8 g + e
-            float s[8];
+        // scores: lane (column m) has tokens t0 + 8 g + e
+        float s[8];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-#pragma unroll
-                for (int q = 0; q < NG; ++q) {
-                    f32x4 x = {cinit[q], cinit[q], cinit[q], cinit[q]};
-#pragma unroll
-                    for (int k = 2 * q; k < 2 * q + 2; ++k) {
-                        const bf16x8 kf = unit_bf16<BITS>(&cur.k[u][k * KU]);
-#pragma unroll
-                        for (int p = 0; p < NP; ++p) x = mfma16(kf, qf[p][k], x);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float ks = scale_of(cur.ks[q], 4 * u + i);
-                        s[4 * u + i] = q == 0 ? x[i] * ks : fmaf(x[i], ks, s[4 * u + i]);
-                    }
-                }
-            }
-            if (a.cap > 0.f) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {           // tanh |y| = (1 - x) / (1 + x), x = exp(-2 |y|)
-                    const float x = __builtin_amdgcn_exp2f(-fabsf(s[e] * cap_mul));
-                    s[e] = copysignf((1.f - x) * __builtin_amdgcn_rcpf(1.f + x), s[e]) * (a.cap * kLog2e);
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) s[e] *= mul;
-            }
-            const bool full = t0 >= lo_all && t0 + 32 <= hi_all;
-            if (a.slopes) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) s[e] -= col.slope * col.distance(a, t0 + 8 * g + e, s0, n, base);
-            }
-            uint32_t vis = 0xFFu;
-            if (!full) {
-                vis = col.sees8(a.tree != nullptr, base, t0 + 8 * g);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) s[e] = (vis >> e) & 1 ? s[e] : neg_inf();
-            }
-            float mx = s[0];
-#pragma unroll
-            for (int e = 1; e < 8; ++e) mx = fmaxf(mx, s[e]);
-            if (__any(mx > mrun + 8.f)) {
-                mx = fmaxf(mx, __shfl_xor(mx, 16));
-                mx = fmaxf(mx, __shfl_xor(mx, 32));
-                mx = fmaxf(mx, mrun);
-                const float alpha = mx == mrun ? 1.f : __builtin_amdgcn_exp2f(mrun - mx);
-                mrun = mx;
-                lrun *= alpha;
-#pragma unroll
-                for (int i = 0; i < NV; ++i) acc[i] *= alpha;
-#pragma unroll
-                for (int q = 0; q < NG; ++q) corr[q] *= alpha;
-            }
-            const float mu = mrun == neg_inf() ? 0.f : mrun;
-            float p[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                p[e] = __builtin_amdgcn_exp2f(s[e] - mu);
-                lrun += p[e];
-            }
+        for (int u = 0; u < 2; ++u) {
 #pragma unroll
             for (int q = 0; q < NG; ++q) {
-                uint32_t wv[4];
+                f32x4 x = {cinit[q], cinit[q], cinit[q], cinit[q]};
+#pragma unroll
+                for (int k = 2 * q; k < 2 * q + 2; ++k) {
+                    const bf16x8 kf = unit_bf16<BITS>(&use.k[u][k * KU]);
+#pragma unroll
+                    for (int p = 0; p < NP; ++p) x = mfma16(kf, qf[p][k], x);
+                }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    float w0 = p[2 * i] * scale_of(cur.vs[q], 2 * i), w1 = p[2 * i + 1] * scale_of(cur.vs[q], 2 * i + 1);
-                    if (!full) {                        // a masked token's scale may be anything
-                        w0 = (vis >> (2 * i)) & 1 ? w0 : 0.f;
-                        w1 = (vis >> (2 * i + 1)) & 1 ? w1 : 0.f;
-                    }
-                    wv[i] = bf16_pair(w0, w1);
+                    const float ks = scale_of(use.ks[q], 4 * u + i);
+                    s[4 * u + i] = q == 0 ? x[i] * ks : fmaf(x[i], ks, s[4 * u + i]);
                 }
-                const bf16x8 wf = __builtin_bit_cast(bf16x8, make_uint4(wv[0], wv[1], wv[2], wv[3]));
-                corr[q] = mfma16(ones, wf, corr[q]);
-#pragma unroll
-                for (int i = q * (NV / NG); i < (q + 1) * (NV / NG); ++i)
-                    acc[i] = mfma16(unit_bf16<BITS>(&cur.v[i * KU]), wf, acc[i]);
             }
         }
-        cur = nxt;
-        page = pnext;
+        if (a.cap > 0.f) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {           // tanh |y| = (1 - x) / (1 + x), x = exp(-2 |y|)
+                const float x = __builtin_amdgcn_exp2f(-fabsf(s[e] * cap_mul));
+                s[e] = copysignf((1.f - x) * __builtin_amdgcn_rcpf(1.f + x), s[e]) * (a.cap * kLog2e);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[e] *= mul;
+        }
+        const bool full = t0 >= lo_all && t0 + 32 <= hi_all;
+        if (a.slopes) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[e] -= col.slope * col.distance(a, t0 + 8 * g + e, s0, n, base);
+        }
+        uint32_t vis = 0xFFu;
+        if (!full) {
+            vis = col.sees8(a.tree != nullptr, base, t0 + 8 * g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[e] = (vis >> e) & 1 ? s[e] : neg_inf();
+        }
+        float mx = s[0];
+#pragma unroll
+        for (int e = 1; e < 8; ++e) mx = fmaxf(mx, s[e]);
+        if (__any(mx > mrun + 8.f)) {
+            mx = fmaxf(mx, __shfl_xor(mx, 16));
+            mx = fmaxf(mx, __shfl_xor(mx, 32));
+            mx = fmaxf(mx, mrun);
+            const float alpha = mx == mrun ? 1.f : __builtin_amdgcn_exp2f(mrun - mx);
+            mrun = mx;
+            lrun *= alpha;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) acc[i] *= alpha;
+#pragma unroll
+            for (int q = 0; q < NG; ++q) corr[q] *= alpha;
+        }
+        const float mu = mrun == neg_inf() ? 0.f : mrun;
+        float p[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            p[e] = __builtin_amdgcn_exp2f(s[e] - mu);
+            lrun += p[e];
+        }
+#pragma unroll
+        for (int q = 0; q < NG; ++q) {
+            uint32_t wv[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float w0 = p[2 * i] * scale_of(use.vs[q], 2 * i), w1 = p[2 * i + 1] * scale_of(use.vs[q], 2 * i + 1);
+                if (!full) {                        // a masked token's scale may be anything
+                    w0 = (vis >> (2 * i)) & 1 ? w0 : 0.f;
+                    w1 = (vis >> (2 * i + 1)) & 1 ? w1 : 0.f;
+                }
+                wv[i] = bf16_pair(w0, w1);
+            }
+            const bf16x8 wf = __builtin_bit_cast(bf16x8, make_uint4(wv[0], wv[1], wv[2], wv[3]));
+            corr[q] = mfma16(ones, wf, corr[q]);
+#pragma unroll
+            for (int i = q * (NV / NG); i < (q + 1) * (NV / NG); ++i)
+                acc[i] = mfma16(unit_bf16<BITS>(&use.v[i * KU]), wf, acc[i]);
+        }
+    };
+    for (int blk = bs + wave; blk < be; blk += 2 * kWaves) {
+        int next = page_of(blk + kWaves);
+        load(odd, blk + kWaves, next);
+        if (page >= 0) work(even, blk);
+        page = next;
+        next = page_of(blk + 2 * kWaves);
+        load(even, blk + 2 * kWaves, next);
+        if (page >= 0) work(odd, blk + kWaves);
+        page = next;
     }
 
     // ---- join the waves
@@ -384,63 +404,93 @@ __global__ __launch_bounds__(64 * kWaves) void k_cache_attn(CacheAttnArgs a, int
     }
 }
 
-// One workgroup of 256 threads per (query row, head): 2048 / D groups of D / 8
-// lanes take the splits in turn and are joined through LDS.
+// ---------------------------------------------------------------- joining token ranges
+// o = sum_s 2^(m_s - m) o_s, l likewise, over the ranges s of a row; a range in
+// which the row saw nothing (m_s = -inf) has no sums in the workspace.  Rows are
+// addressed through the sequences, so rows that no sequence has stay as they are.
+
+// Up to kFew ranges: D / 8 lanes take a row's ranges one after the other.
+constexpr int kFew = 16;
 template <int D, bool ROT>
-__global__ __launch_bounds__(256) void k_cache_attn_join(CacheAttnArgs a) {
+__global__ __launch_bounds__(256) void k_cache_attn_join(CacheAttnArgs a, int nblk) {
     constexpr int NGRP = 2048 / D;
-    const int head = blockIdx.x % a.hq, row = blockIdx.x / a.hq;
-    // rows that no sequence of the call has are left as they are
-    __shared__ int owned;
-    __shared__ float so[NGRP][D], sl[NGRP], sm[NGRP];
-    const int tid = threadIdx.x, grp = tid / (D / 8), j = tid % (D / 8);
-    if (tid == 0) owned = 0;
-    __syncthreads();
-    for (int b = tid; b < a.c.batch; b += 256) {
-        int s0;
-        const int n = min(ragged_rows(a.starts, b, a.total, &s0), a.max_q);
-        if (row >= s0 && row < s0 + n) owned = 1;
-    }
-    __syncthreads();
-    if (!owned) return;
+    const int b = blockIdx.x / nblk, blk = blockIdx.x % nblk;
+    int s0;
+    const int n = min(ragged_rows(a.starts, b, a.total, &s0), a.max_q);
+    const int grp = threadIdx.x / (D / 8), j = threadIdx.x % (D / 8), r = blk * NGRP + grp;
+    if (blk * NGRP >= n * a.hq) return;
+    const bool on = r < n * a.hq;
+    const int row = s0 + (on ? r / a.hq : 0), head = on ? r % a.hq : 0;
     const int64_t rows = (int64_t)a.total * a.hq, at = (int64_t)row * a.hq + head;
     float m = neg_inf(), l = 0.f, o[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) o[e] = 0.f;
-    for (int s = grp; s < a.splits; s += NGRP) {
-        const float ms = a.ws_ml[2 * (s * rows + at)], ls = a.ws_ml[2 * (s * rows + at) + 1];
-        if (ms == neg_inf()) continue;
-        const float mn = fmaxf(m, ms);
-        const float f0 = m == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(m - mn), f1 = __builtin_amdgcn_exp2f(ms - mn);
+#pragma unroll 4
+    for (int s = 0; s < a.splits; ++s) {
+        const float2 ml = *reinterpret_cast<const float2 *>(a.ws_ml + 2 * (s * rows + at));
         const float4 *p = reinterpret_cast<const float4 *>(a.ws_part + (s * rows + at) * D + 8 * j);
         const float4 x = p[0], y = p[1];
         const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        const bool none = ml.x == neg_inf();
+        const float mn = fmaxf(m, ml.x);
+        const float f0 = m == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(m - mn), f1 = none ? 0.f : __builtin_amdgcn_exp2f(ml.x - mn);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = fmaf(o[e], f0, v[e] * f1);
-        l = fmaf(l, f0, ls * f1);
+        for (int e = 0; e < 8; ++e) o[e] = fmaf(o[e], f0, none ? 0.f : v[e] * f1);
+        l = fmaf(l, f0, none ? 0.f : ml.y * f1);
         m = mn;
+    }
+    finish_row<D, ROT>(a, row, head, j, o, m, l, on);
+}
+
+// More: one workgroup of 256 threads per row.  Every thread first takes one
+// range's m and l, so that all weights are known after one read; then 2048 / D
+// groups of D / 8 lanes sum the ranges in turn and are added through LDS.
+constexpr int kMaxSplits = 256;
+template <int D, bool ROT>
+__global__ __launch_bounds__(256) void k_cache_attn_join_many(CacheAttnArgs a) {
+    constexpr int NGRP = 2048 / D;
+    const int b = blockIdx.x / (a.max_q * a.hq), r = blockIdx.x % (a.max_q * a.hq);
+    int s0;
+    const int n = min(ragged_rows(a.starts, b, a.total, &s0), a.max_q);
+    if (r >= n * a.hq) return;
+    const int row = s0 + r / a.hq, head = r % a.hq, tid = threadIdx.x;
+    const int64_t rows = (int64_t)a.total * a.hq, at = (int64_t)row * a.hq + head;
+    __shared__ float so[NGRP][D + 4], sw[kMaxSplits], red[2][4];
+    const float2 ml = tid < a.splits ? *reinterpret_cast<const float2 *>(a.ws_ml + 2 * (tid * rows + at))
+                                     : make_float2(neg_inf(), 0.f);
+    const float mw = wave_max(ml.x);
+    if ((tid & 63) == 0) red[0][tid >> 6] = mw;
+    __syncthreads();
+    const float m = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+    const float w = ml.x == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(ml.x - m);
+    sw[tid] = w;
+    const float lw = wave_sum(w == 0.f ? 0.f : w * ml.y);
+    if ((tid & 63) == 0) red[1][tid >> 6] = lw;
+    __syncthreads();
+    const float l = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+    const int grp = tid / (D / 8), j = tid % (D / 8);
+    float o[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = 0.f;
+#pragma unroll 4
+    for (int s = grp; s < a.splits; s += NGRP) {
+        const float4 *p = reinterpret_cast<const float4 *>(a.ws_part + (s * rows + at) * D + 8 * j);
+        const float4 x = p[0], y = p[1];
+        const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w}, f = sw[s];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] += f == 0.f ? 0.f : v[e] * f;
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) so[grp][8 * j + e] = o[e];
-    if (j == 0) {
-        sm[grp] = m;
-        sl[grp] = l;
-    }
     __syncthreads();
     if (tid >= 64) return;                              // one wave (whole, for the lane exchanges) finishes the row
     const int jj = tid % (D / 8);
-    float mt = neg_inf(), lt = 0.f, ot[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ot[e] = 0.f;
-    for (int x = 0; x < NGRP; ++x) mt = fmaxf(mt, sm[x]);
-    for (int x = 0; x < NGRP; ++x) {
-        if (sm[x] == neg_inf()) continue;
-        const float f = __builtin_amdgcn_exp2f(sm[x] - mt);
-        lt = fmaf(sl[x], f, lt);
+    for (int e = 0; e < 8; ++e) o[e] = 0.f;
+    for (int x = 0; x < NGRP; ++x)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ot[e] = fmaf(so[x][8 * jj + e], f, ot[e]);
-    }
-    finish_row<D, ROT>(a, row, head, jj, ot, mt, lt, tid < D / 8);
+        for (int e = 0; e < 8; ++e) o[e] += so[x][8 * jj + e];
+    finish_row<D, ROT>(a, row, head, jj, o, m, l, tid < D / 8);
 }
 
 // ---------------------------------------------------------------- launchers
@@ -460,11 +510,17 @@ static hipError_t attn_d(const CacheAttnArgs &a, bool wide, int bits, bool rotat
     else if (bits == 4) e = rotate ? attn_launch<D, 4, true>(a, s) : attn_launch<D, 4, false>(a, s);
     else e = rotate ? attn_launch<D, 8, true>(a, s) : attn_launch<D, 8, false>(a, s);
     if (e != hipSuccess || a.splits == 1) return e;
-    const int64_t rows = (int64_t)a.total * a.hq;
-    if (rows > 0x7FFFFFFF) return hipErrorInvalidValue;
+    const int64_t rows = (int64_t)a.max_q * a.hq, many = rows * a.c.batch, nblk = (rows * D + 2047) / 2048;
+    if (many > 0x7FFFFFFF) return hipErrorInvalidValue;
     KTimeScope kts("k_cache_attn_join", s);
-    if (rotate) hipLaunchKernelGGL((k_cache_attn_join<D, true>), dim3((unsigned)rows), dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((k_cache_attn_join<D, false>), dim3((unsigned)rows), dim3(256), 0, s, a);
+    const dim3 gf((unsigned)(nblk * a.c.batch)), gm((unsigned)many), t(256);
+    if (a.splits <= kFew) {
+        if (rotate) hipLaunchKernelGGL((k_cache_attn_join<D, true>), gf, t, 0, s, a, (int)nblk);
+        else hipLaunchKernelGGL((k_cache_attn_join<D, false>), gf, t, 0, s, a, (int)nblk);
+    } else {
+        if (rotate) hipLaunchKernelGGL((k_cache_attn_join_many<D, true>), gm, t, 0, s, a);
+        else hipLaunchKernelGGL((k_cache_attn_join_many<D, false>), gm, t, 0, s, a);
+    }
     return hipGetLastError();
 }
 hipError_t launch_cache_attention(const CacheAttnArgs &a, bool wide, int d, int bits, bool rotate, hipStream_t s) {

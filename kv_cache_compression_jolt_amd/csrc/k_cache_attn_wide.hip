@@ -221,7 +221,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
     end = __builtin_amdgcn_readfirstlane(end);
     lo_any = __builtin_amdgcn_readfirstlane(lo_any);
     const int tile0 = begin / kTile, ntile = end > begin ? (end + kTile - 1) / kTile - tile0 : 0;
-    const int per = (ntile + a.splits - 1) / a.splits;
+    const int per = max((ntile + a.splits - 1) / a.splits, a.least / kTile);
     const int ts = tile0 + split * per, te = min(ts + per, tile0 + ntile);
 
     const int P = 1 << a.c.page_shift;
