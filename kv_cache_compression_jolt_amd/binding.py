@@ -516,56 +516,54 @@ class JoltCache:
         with torch.cuda.device(self.device):
             self.h = jolt_create(self.device.index)
 
-    def _tensor(self, name, t, dtype, dims=None):
-        if t.dtype != dtype or t.device != self.device or not t.is_contiguous() or \
-                (dims is not None and t.dim() != dims):
-            raise ValueError("%s must be a contiguous %s tensor%s on %s"
-                             % (name, dtype, "" if dims is None else " of %d dimensions" % dims, self.device))
+    def _tensor(self, name, t, dtype, dims=None, numel=None):
+        if t.dtype is not dtype or t.device != self.device or not t.is_contiguous() or \
+                (dims is not None and t.dim() != dims) or (numel is not None and t.numel() != numel):
+            raise ValueError("%s must be a contiguous %s tensor%s%s on %s"
+                             % (name, dtype, "" if dims is None else " of %d dimensions" % dims,
+                                "" if numel is None else " of %d entries" % numel, self.device))
         return t.data_ptr()
 
-    def _starts(self, starts):
-        if starts.numel() != self.batch + 1:
-            raise ValueError("starts must have batch + 1 entries")
-        return self._tensor("starts", starts, self.torch.int32)
-
-    def _rows(self, name, t, heads, dtypes):
-        if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != self.d or t.dtype not in dtypes \
-                or t.device != self.device or (t.stride(2) != 1 and t.numel()):
-            raise ValueError("%s must be [rows, %d, %d] with contiguous features, of %s, on %s"
-                             % (name, heads, self.d, " or ".join(map(str, dtypes)), self.device))
-        return jolt_rows(t.data_ptr(), t.stride(0), t.stride(1))
+    def _rows(self, name, t, heads):
+        shape, stride = t.shape, t.stride()
+        if len(shape) != 3 or shape[1] != heads or shape[2] != self.d or stride[2] != 1 or t.device != self.device:
+            raise ValueError("%s must be [rows, %d, %d] with contiguous features on %s"
+                             % (name, heads, self.d, self.device))
+        return jolt_rows(t.data_ptr(), stride[0], stride[1])
 
     def _kv(self, k, v):
-        dt = (self.torch.bfloat16, self.torch.float32)
-        rk, rv = self._rows("k", k, self.H, dt), self._rows("v", v, self.H, dt)
-        if k.dtype != v.dtype or k.shape[0] != v.shape[0]:
+        rk, rv, dt = self._rows("k", k, self.H), self._rows("v", v, self.H), k.dtype
+        if v.dtype is not dt or k.shape[0] != v.shape[0]:
             raise ValueError("k and v differ in dtype or rows")
-        return rk, rv, JOLT_F32 if k.dtype == self.torch.float32 else JOLT_BF16
+        if dt is self.torch.bfloat16:
+            return rk, rv, JOLT_BF16
+        if dt is self.torch.float32:
+            return rk, rv, JOLT_F32
+        raise ValueError("k and v must be bfloat16 or float32")
 
     def _stream(self):
-        return self.torch.cuda.current_stream(self.device).cuda_stream
+        return self.torch._C._cuda_getCurrentRawStream(self.device.index)
 
     def append(self, k, v, starts, max_new):
         """Write rows k, v [total, H, d] (bf16 or fp32) as the last tokens of their sequences."""
         rk, rv, dt = self._kv(k, v)
-        jolt_cache_append(self.h, self.c, self.batch, self._starts(starts), k.shape[0], max_new, dt, rk, rv,
-                          self._stream())
+        jolt_cache_append(self.h, self.c, self.batch, self._tensor("starts", starts, self.torch.int32, 1, self.batch + 1),
+                          k.shape[0], max_new, dt, rk, rv, self._stream())
 
     def read(self, first, starts, max_rows, k, v):
         """Read tokens first[b] .. of every sequence into k, v [total, H, d] (bf16 or fp32)."""
         rk, rv, dt = self._kv(k, v)
-        if first is not None and first.numel() != self.batch:
-            raise ValueError("first must have batch entries")
-        fp = None if first is None else self._tensor("first", first, self.torch.int32)
-        jolt_cache_read(self.h, self.c, self.batch, fp, self._starts(starts), k.shape[0], max_rows, dt, rk, rv,
-                        self._stream())
+        i32 = self.torch.int32
+        fp = None if first is None else self._tensor("first", first, i32, 1, self.batch)
+        jolt_cache_read(self.h, self.c, self.batch, fp, self._tensor("starts", starts, i32, 1, self.batch + 1),
+                        k.shape[0], max_rows, dt, rk, rv, self._stream())
 
     def keep(self, base, starts, path):
         """Move drafted tokens base[b] + path[i] of every sequence to base[b] + 0, 1, ..."""
-        if base.numel() != self.batch:
-            raise ValueError("base must have batch entries")
-        jolt_cache_keep(self.h, self.c, self.batch, self._tensor("base", base, self.torch.int32), self._starts(starts),
-                        self._tensor("path", path, self.torch.int32), path.numel(), self._stream())
+        i32 = self.torch.int32
+        jolt_cache_keep(self.h, self.c, self.batch, self._tensor("base", base, i32, 1, self.batch),
+                        self._tensor("starts", starts, i32, 1, self.batch + 1), self._tensor("path", path, i32, 1),
+                        path.numel(), self._stream())
 
     def workspace_bytes(self, total, max_q, max_len, q_heads) -> int:
         return jolt_cache_attention_workspace_size(self.c, self.batch, total, max_q, max_len, q_heads)
@@ -573,55 +571,61 @@ class JoltCache:
     def _attend(self, q, starts, max_q, max_len, tree, out, lse, scale, cap, slopes, window, prefix, first, merge_out,
                 merge_lse, workspace):
         torch = self.torch
+        f32, i32, bf16 = torch.float32, torch.int32, torch.bfloat16
         total, hq = q.shape[0], q.shape[1]
-        rq, ro = self._rows("q", q, hq, (torch.bfloat16,)), self._rows("out", out, hq, (torch.bfloat16,))
-        if out.shape[0] != total:
-            raise ValueError("q and out differ in rows")
-        t = jolt_attn_terms(scale, cap, window, 0)
-        f32, i32 = torch.float32, torch.int32
-        for name, x, dt, numel in (("slopes", slopes, f32, hq), ("prefix", prefix, i32, self.batch),
-                                   ("first", first, i32, total), ("merge_out", merge_out, f32, total * hq * self.d),
-                                   ("merge_lse", merge_lse, f32, total * hq)):
-            if x is not None:
-                if x.numel() != numel:
-                    raise ValueError("%s must have %d entries" % (name, numel))
-                setattr(t, name, self._tensor(name, x, dt))
-        if lse is not None and lse.numel() != total * hq:
-            raise ValueError("lse must be [rows, q_heads]")
-        lp = None if lse is None else self._tensor("lse", lse, f32)
-        need = self.workspace_bytes(total, max_q, max_len, hq)
+        rq, ro = self._rows("q", q, hq), self._rows("out", out, hq)
+        if q.dtype is not bf16 or out.dtype is not bf16 or out.shape[0] != total:
+            raise ValueError("q and out must be bfloat16 and have the same rows")
+        t = jolt_attn_terms(self.d ** -0.5 if scale is None else scale, cap, window, 0)
+        if slopes is not None:
+            t.slopes = self._tensor("slopes", slopes, f32, None, hq)
+        if prefix is not None:
+            t.prefix = self._tensor("prefix", prefix, i32, None, self.batch)
+        if first is not None:
+            t.first = self._tensor("first", first, i32, None, total)
+        if merge_out is not None:
+            t.merge_out = self._tensor("merge_out", merge_out, f32, None, total * hq * self.d)
+        if merge_lse is not None:
+            t.merge_lse = self._tensor("merge_lse", merge_lse, f32, None, total * hq)
+        lp = None if lse is None else self._tensor("lse", lse, f32, None, total * hq)
+        sp = self._tensor("starts", starts, i32, 1, self.batch + 1)
         stream = self._stream()
-        if workspace is None:
-            if need:
-                # none is dropped: a captured graph goes on using the one it was captured with
-                have = self.workspaces.setdefault(stream, [])
-                if not have or have[-1].numel() < need:
-                    have.append(torch.empty(need, dtype=torch.uint8, device=self.device))
-                workspace = have[-1]
-        elif workspace.device != self.device or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        own = workspace is None
+        if own:
+            have = self.workspaces.get(stream)
+            workspace = have[-1] if have else None
+        elif workspace.device != self.device or workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous uint8 tensor on %s" % (self.device,))
-        wp, wb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
-        sp = self._starts(starts)
-        if tree is None:
-            jolt_cache_attention(self.h, self.c, self.batch, sp, total, max_q, max_len, hq, rq, t, ro, lp, wp, wb,
-                                 stream)
-        else:
-            if tree.numel() != total:
-                raise ValueError("tree must have one mask for each row")
-            jolt_tree_attention(self.h, self.c, self.batch, sp, total, max_q, max_len, hq, rq,
-                                self._tensor("tree", tree, torch.int64), t, ro, lp, wp, wb, stream)
+        if tree is not None:
+            tp = self._tensor("tree", tree, torch.int64, None, total)
+        for again in (False, True):
+            wp, wb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+            if tree is None:
+                st = lib().jolt_cache_attention(self.h, self.c, self.batch, sp, total, max_q, max_len, hq, rq, t, ro,
+                                                lp, wp, wb, stream)
+            else:
+                st = lib().jolt_tree_attention(self.h, self.c, self.batch, sp, total, max_q, max_len, hq, rq, tp, t,
+                                               ro, lp, wp, wb, stream)
+            if st != JOLT_E_WORKSPACE or not own or again:
+                break
+            # refused before any launch: a larger workspace, and again.  None is
+            # dropped: a captured graph goes on using the one it was captured with
+            workspace = torch.empty(self.workspace_bytes(total, max_q, max_len, hq), dtype=torch.uint8,
+                                    device=self.device)
+            self.workspaces.setdefault(stream, []).append(workspace)
+        _check(st, self.h)
 
     def attention(self, q, starts, max_q, max_len, out, lse=None, scale=None, cap=0.0, slopes=None, window=0,
                   prefix=None, first=None, merge_out=None, merge_lse=None, workspace=None):
         """Attention of q [total, q_heads, d] (bf16) over the cache into out (bf16) and lse (fp32)."""
-        self._attend(q, starts, max_q, max_len, None, out, lse, self.d ** -0.5 if scale is None else scale, cap,
-                     slopes, window, prefix, first, merge_out, merge_lse, workspace)
+        self._attend(q, starts, max_q, max_len, None, out, lse, scale, cap, slopes, window, prefix, first,
+                     merge_out, merge_lse, workspace)
 
     def tree_attention(self, q, starts, max_q, max_len, tree, out, lse=None, scale=None, cap=0.0, slopes=None,
                        window=0, prefix=None, first=None, merge_out=None, merge_lse=None, workspace=None):
         """The same for drafted tokens: tree (int64 bit masks, one a row) says which slots a row sees."""
-        self._attend(q, starts, max_q, max_len, tree, out, lse, self.d ** -0.5 if scale is None else scale, cap,
-                     slopes, window, prefix, first, merge_out, merge_lse, workspace)
+        self._attend(q, starts, max_q, max_len, tree, out, lse, scale, cap, slopes, window, prefix, first,
+                     merge_out, merge_lse, workspace)
 
     def close(self):
         if self.h is not None:

@@ -73,6 +73,8 @@ __device__ __forceinline__ uint2 member_mask(int e) {
     else return e < 4 ? make_uint2(255u << (8 * e), 0) : make_uint2(0, 255u << (8 * (e - 4)));
 }
 
+typedef short s16x2 __attribute__((ext_vector_type(2)));
+
 struct BlockId { int b, blk, h; };
 __device__ __forceinline__ BlockId block_id(int64_t w, int H, int nblk) {
     BlockId r;
@@ -193,10 +195,82 @@ __global__ __launch_bounds__(D) void k_cache_append(CacheRowsArgs a, int nblk) {
 }
 
 // ---------------------------------------------------------------- read
-// The same mapping backwards: thread (row r, lane j) rebuilds features
-// 8 j .. 8 j + 7 of one token.  The rotation of a group's integer codes is
-// exact in fp32 (at most 64 * 127), so a value is isd (s0 I0 +- s1 I1) with
-// three roundings.
+// A thread (row r, lane j of D / 8) rebuilds features 8 j .. 8 j + 7 of one token
+// of a block of 8, and does so for kReadBlocks blocks at once, so that their
+// loads are in flight together.  The rotation of a group of 64 works on the
+// unsigned codes as packed 16-bit integers, two features to an instruction (at
+// most 64 * 255); their offset only reaches the group's feature 0, as 64 times
+// itself.  It is exact, so a value is s0 I0 +- s1 I1 with the scales times isd:
+// four roundings.
+constexpr int kReadBlocks = 2;
+
+// codes of features 8 j .. 8 j + 7 as 16-bit pairs (2 i, 2 i + 1)
+template <int BITS>
+__device__ __forceinline__ void key_codes(const uint8_t *codes, int64_t unit, s16x2 (&x)[4]) {
+    const uint2 w = load_unit<BITS>(codes, unit);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t u;
+        if constexpr (BITS == 4) u = (w.x >> (4 * i)) & 0x000F000Fu;
+        else u = __builtin_amdgcn_perm(0, i < 2 ? w.x : w.y, (i & 1) ? 0x0C030C02u : 0x0C010C00u);
+        x[i] = __builtin_bit_cast(s16x2, u);
+    }
+}
+// member e of the units of 8 consecutive features
+template <int BITS>
+__device__ __forceinline__ void value_codes(const uint8_t *codes, int64_t unit, int e, s16x2 (&x)[4]) {
+    uint32_t w[8];
+    if constexpr (BITS == 4) {
+        const uint4 *p = reinterpret_cast<const uint4 *>(codes + unit * 4);
+        const uint4 a = p[0], b = p[1];
+        w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+        w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+    } else {
+        const uint4 *p = reinterpret_cast<const uint4 *>(codes + unit * 8);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint4 a = p[i];
+            w[2 * i] = e < 4 ? a.x : a.y;
+            w[2 * i + 1] = e < 4 ? a.z : a.w;
+        }
+    }
+    const int sh = BITS == 4 ? nibble_of(e) : 8 * (e & 3);
+    constexpr uint32_t mask = BITS == 4 ? 15u : 255u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        x[i] = __builtin_bit_cast(s16x2, ((w[2 * i] >> sh) & mask) | (((w[2 * i + 1] >> sh) & mask) << 16));
+}
+template <int X>
+__device__ __forceinline__ s16x2 lane_xor_pair(s16x2 v) {
+    return __builtin_bit_cast(s16x2, __float_as_uint(lane_xor<X>(__uint_as_float(__builtin_bit_cast(uint32_t, v)))));
+}
+template <int X>
+__device__ __forceinline__ void fwht_pairs_lane(s16x2 (&x)[4], int j) {
+    const short s = (j & X) ? -1 : 1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const s16x2 o = lane_xor_pair<X>(x[i]);
+        x[i] = x[i] * s16x2{s, s} + o;
+    }
+}
+// the 64-point transform over 8 lanes of 8 features each
+__device__ __forceinline__ void fwht_pairs(s16x2 (&x)[4], int j) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = s16x2{x[i].y, x[i].y} * s16x2{1, -1} + s16x2{x[i].x, x[i].x};
+#pragma unroll
+    for (int h = 1; h < 4; h *= 2)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (!(i & h)) {
+                const s16x2 a = x[i], b = x[i + h];
+                x[i] = a + b;
+                x[i + h] = a - b;
+            }
+    fwht_pairs_lane<1>(x, j);
+    fwht_pairs_lane<2>(x, j);
+    fwht_pairs_lane<4>(x, j);
+}
+
 template <typename T, int D, int BITS, bool ROT>
 __global__ __launch_bounds__(D) void k_cache_read(CacheRowsArgs a, int nblk) {
     const BlockId id = block_id(blockIdx.x, a.c.H, nblk);
@@ -204,63 +278,73 @@ __global__ __launch_bounds__(D) void k_cache_read(CacheRowsArgs a, int nblk) {
     const int n = min(ragged_rows(a.starts, id.b, a.total, &s0), a.max_rows);
     if (n == 0) return;
     const int64_t f0 = a.first ? a.first[id.b] : 0;
-    const int64_t tok8 = ((f0 >> 3) + id.blk) * 8;
+    const int64_t tok8 = ((f0 >> 3) + id.blk * kReadBlocks) * 8;
     if (tok8 >= f0 + n) return;
     const int len = cache_len(a.c, id.b);
-    const int page = tok8 >= 0 && tok8 < len ? cache_page(a.c, id.b, (int)tok8) : -1;
     const int tid = threadIdx.x, j = tid % (D / 8), r = tid / (D / 8);
-    const int64_t t = tok8 + r;
-    const bool on = t >= f0 && t < f0 + n, have = page >= 0 && t < len;
-    const uint8_t *base = a.c.pool + cache_block_offset(a.c, max(page, 0), id.h);
-    const int P = 1 << a.c.page_shift, tin = (int)(tok8 & (P - 1));
+    const int P = 1 << a.c.page_shift;
     const PageLayout pl = page_layout(P, D, BITS);
-    constexpr float off = (float)(1 << (BITS - 1));
-    __shared__ __align__(16) uint8_t vc[8][D];
-    if (page >= 0) {
-        const uint2 w = load_unit<BITS>(base + pl.v_codes, (int64_t)(tin >> 3) * D + tid);
+    constexpr int off = 1 << (BITS - 1);
+    s16x2 x[kReadBlocks][2][4];
+    float sc[kReadBlocks][2];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) vc[e][tid] = (uint8_t)unit_code<BITS>(w, e);
-    }
-    __syncthreads();
+    for (int i = 0; i < kReadBlocks; ++i) {
+        const int64_t t = tok8 + 8 * i;
+        const int page = t >= 0 && t < len ? cache_page(a.c, id.b, (int)t) : -1;
+        const bool have = page >= 0 && t + r < len;
+        const uint8_t *base = a.c.pool + cache_block_offset(a.c, max(page, 0), id.h);
+        const int tin = (int)(t & (P - 1));
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-        float x[8];
+        for (int kv = 0; kv < 2; ++kv) {
+            sc[i][kv] = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = 0.f;
-        float sc = 0.f;
+            for (int e = 0; e < 4; ++e) x[i][kv][e] = s16x2{off, off};
+            if (have)
+                sc[i][kv] = bf16_to_f32(reinterpret_cast<const uint16_t *>(base + (kv ? pl.v_scales : pl.k_scales))[(j >> 3) * P + tin + r]);
+        }
         if (have) {
-            uint2 w;
-            if (kv == 0) {
-                w = load_unit<BITS>(base, (int64_t)(tin + r) * (D / 8) + (j & 3) * (D / 32) + (j >> 2));
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = (float)unit_code<BITS>(w, e) - off;
-            } else {
-                w = *reinterpret_cast<const uint2 *>(&vc[r][8 * j]);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = (float)unit_code<8>(w, e) - off;
-            }
-            sc = bf16_to_f32(reinterpret_cast<const uint16_t *>(base + (kv ? pl.v_scales : pl.k_scales))[(j >> 3) * P + tin + r]);
+            key_codes<BITS>(base, (int64_t)(tin + r) * (D / 8) + (j & 3) * (D / 32) + (j >> 2), x[i][0]);
+            value_codes<BITS>(base + pl.v_codes, (int64_t)(tin >> 3) * D + 8 * j, r, x[i][1]);
         }
-        if constexpr (ROT) {
-            fwht_row<64>(x, j);
-            const uint32_t sb = sign_byte(kv ? a.c.sv : a.c.sk, j);
-            const float isd = D == 128 ? 0.08838834764831845f : 0.125f;
+    }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                x[e] *= sc;
+    for (int i = 0; i < kReadBlocks; ++i) {
+        const int64_t t = tok8 + 8 * i + r;
+        const bool on = t >= f0 && t < f0 + n;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+            s16x2(&w)[4] = x[i][kv];
+            float y[8];
+            if constexpr (ROT) {
+                fwht_pairs(w, j);
+                if ((j & 7) == 0) w[0].x -= 64 * off;
+                const float s = sc[i][kv] * (D == 128 ? 0.08838834764831845f : 0.125f);
+                const uint32_t sb = sign_byte(kv ? a.c.sv : a.c.sk, j);
+                s16x2 o[4];
+                float so = 0.f;
                 if constexpr (D == 128) {
-                    const float o = lane_xor<8>(x[e]);
-                    x[e] = (j & 8) ? o - x[e] : x[e] + o;
-                }
-                x[e] = flip(x[e] * isd, (sb >> e) & 1);
-            }
-        } else {
+                    // feature f + 64 of the row is I0 - I1 where f is I0 + I1
+                    so = lane_xor<8>(s);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] *= sc;
-        }
-        if (on) {
-            const RowsView &dst = kv ? a.v : a.k;
-            store8(static_cast<T *>(dst.ptr) + ((int64_t)s0 + (t - f0)) * dst.ts + id.h * dst.hs + 8 * j, x);
+                    for (int e = 0; e < 4; ++e) o[e] = lane_xor_pair<8>(w[e]);
+                }
+                const float own = (j & 8) ? -s : s;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float v = (float)(e & 1 ? w[e >> 1].y : w[e >> 1].x);
+                    if constexpr (D == 128) y[e] = v * own + (float)(e & 1 ? o[e >> 1].y : o[e >> 1].x) * so;
+                    else y[e] = v * s;
+                    y[e] = flip(y[e], (sb >> e) & 1);
+                }
+            } else {
+                const float s = sc[i][kv], c = -(float)off * s;          // exact: (u - off) s in one rounding
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = fmaf((float)(e & 1 ? w[e >> 1].y : w[e >> 1].x), s, c);
+            }
+            if (on) {
+                const RowsView &dst = kv ? a.v : a.k;
+                store8(static_cast<T *>(dst.ptr) + ((int64_t)s0 + (t - f0)) * dst.ts + id.h * dst.hs + 8 * j, y);
+            }
         }
     }
 }
@@ -351,7 +435,8 @@ static int64_t blocks8(int n) { return ((int64_t)n + 6) / 8 + 1; }
 
 template <typename T, int D, int BITS, bool ROT>
 static hipError_t rows_launch(const CacheRowsArgs &a, bool read, hipStream_t s) {
-    const int64_t nblk = blocks8(a.max_rows), grid = nblk * a.c.H * a.c.batch;
+    const int64_t b8 = blocks8(a.max_rows), nblk = read ? (b8 + kReadBlocks - 1) / kReadBlocks : b8;
+    const int64_t grid = nblk * a.c.H * a.c.batch;
     if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
     if (read) hipLaunchKernelGGL((k_cache_read<T, D, BITS, ROT>), dim3((unsigned)grid), dim3(D), 0, s, a, (int)nblk);
     else hipLaunchKernelGGL((k_cache_append<T, D, BITS, ROT>), dim3((unsigned)grid), dim3(D), 0, s, a, (int)nblk);
