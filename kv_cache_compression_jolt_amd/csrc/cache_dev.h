@@ -8,12 +8,18 @@ namespace jolt {
 
 constexpr int kDppQuadReverse = 0x1B;   // quad_perm [3, 2, 1, 0]
 
-__device__ __forceinline__ float lane_xor1(float v) { return dpp_move<kDppXor1>(v); }
-__device__ __forceinline__ float lane_xor2(float v) { return dpp_move<kDppXor2>(v); }
+// a lane move inside rows of 16 whose source lane always exists (so no old value
+// is kept for it)
+template <int Ctrl>
+__device__ __forceinline__ float row_move(float v) {
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), Ctrl, 0xF, 0xF, true));
+}
+__device__ __forceinline__ float lane_xor1(float v) { return row_move<kDppXor1>(v); }
+__device__ __forceinline__ float lane_xor2(float v) { return row_move<kDppXor2>(v); }
 // i ^ 7 (half mirror), then i ^ 3
-__device__ __forceinline__ float lane_xor4(float v) { return dpp_move<kDppQuadReverse>(dpp_move<kDppHalfMirror>(v)); }
+__device__ __forceinline__ float lane_xor4(float v) { return row_move<kDppQuadReverse>(row_move<kDppHalfMirror>(v)); }
 // i ^ 15 (row mirror), then i ^ 7
-__device__ __forceinline__ float lane_xor8(float v) { return dpp_move<kDppHalfMirror>(dpp_move<kDppMirror>(v)); }
+__device__ __forceinline__ float lane_xor8(float v) { return row_move<kDppHalfMirror>(row_move<kDppMirror>(v)); }
 
 template <int X>
 __device__ __forceinline__ float lane_xor(float v) {

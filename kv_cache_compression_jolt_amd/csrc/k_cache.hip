@@ -28,14 +28,23 @@ template <> __device__ __forceinline__ void load8<float>(const float *p, float (
     x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
     x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
 }
-template <typename T> __device__ __forceinline__ void store8(T *p, const float (&x)[8]);
-template <> __device__ __forceinline__ void store8<uint16_t>(uint16_t *p, const float (&x)[8]) {
-    *reinterpret_cast<uint4 *>(p) =
-        make_uint4(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7]));
+// store 8 values, the sign of value e changed where bit e of `neg` is set
+template <typename T> __device__ __forceinline__ void store8(T *p, const float (&x)[8], uint32_t neg);
+template <> __device__ __forceinline__ void store8<uint16_t>(uint16_t *p, const float (&x)[8], uint32_t neg) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t two = neg >> (2 * i);
+        w[i] = bf16_pair(x[2 * i], x[2 * i + 1]) ^ (((two & 1u) << 15) | ((two & 2u) << 30));
+    }
+    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
-template <> __device__ __forceinline__ void store8<float>(float *p, const float (&x)[8]) {
-    reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+template <> __device__ __forceinline__ void store8<float>(float *p, const float (&x)[8], uint32_t neg) {
+    float y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(__float_as_uint(x[e]) ^ (((neg >> e) & 1u) << 31));
+    reinterpret_cast<float4 *>(p)[0] = make_float4(y[0], y[1], y[2], y[3]);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(y[4], y[5], y[6], y[7]);
 }
 
 // 8 codes as one unit: 8 bytes, or the 32-bit word of a 4-bit cache (in .x)
@@ -75,13 +84,21 @@ __device__ __forceinline__ uint2 member_mask(int e) {
 
 typedef short s16x2 __attribute__((ext_vector_type(2)));
 
+// Workgroups in the order of the dense rows: heads next to each other where a
+// token's heads are, token blocks where a head's tokens are.
 struct BlockId { int b, blk, h; };
-__device__ __forceinline__ BlockId block_id(int64_t w, int H, int nblk) {
+__device__ __forceinline__ BlockId block_id(const CacheRowsArgs &a, int nblk) {
+    const uint32_t w = blockIdx.x, H = a.c.H, per = nblk * H;
+    const uint32_t in = w % per;
     BlockId r;
-    r.h = (int)(w % H);
-    w /= H;
-    r.blk = (int)(w % nblk);
-    r.b = (int)(w / nblk);
+    r.b = w / per;
+    if (a.k.hs > a.k.ts) {
+        r.h = in / nblk;
+        r.blk = in % nblk;
+    } else {
+        r.blk = in / H;
+        r.h = in % H;
+    }
     return r;
 }
 
@@ -125,7 +142,7 @@ __device__ __forceinline__ uint16_t quantize8(const float (&y)[8], uint32_t (&u)
 // with it every code is independent of the order of the butterflies.
 template <typename T, int D, int BITS, bool ROT>
 __global__ __launch_bounds__(D) void k_cache_append(CacheRowsArgs a, int nblk) {
-    const BlockId id = block_id(blockIdx.x, a.c.H, nblk);
+    const BlockId id = block_id(a, nblk);
     int s0;
     const int n = ragged_rows(a.starts, id.b, a.total, &s0);
     if (n == 0) return;
@@ -273,7 +290,7 @@ __device__ __forceinline__ void fwht_pairs(s16x2 (&x)[4], int j) {
 
 template <typename T, int D, int BITS, bool ROT>
 __global__ __launch_bounds__(D) void k_cache_read(CacheRowsArgs a, int nblk) {
-    const BlockId id = block_id(blockIdx.x, a.c.H, nblk);
+    const BlockId id = block_id(a, nblk);
     int s0;
     const int n = min(ragged_rows(a.starts, id.b, a.total, &s0), a.max_rows);
     if (n == 0) return;
@@ -315,11 +332,12 @@ __global__ __launch_bounds__(D) void k_cache_read(CacheRowsArgs a, int nblk) {
         for (int kv = 0; kv < 2; ++kv) {
             s16x2(&w)[4] = x[i][kv];
             float y[8];
+            uint32_t sb = 0;
             if constexpr (ROT) {
                 fwht_pairs(w, j);
                 if ((j & 7) == 0) w[0].x -= 64 * off;
                 const float s = sc[i][kv] * (D == 128 ? 0.08838834764831845f : 0.125f);
-                const uint32_t sb = sign_byte(kv ? a.c.sv : a.c.sk, j);
+                sb = sign_byte(kv ? a.c.sv : a.c.sk, j);
                 s16x2 o[4];
                 float so = 0.f;
                 if constexpr (D == 128) {
@@ -332,9 +350,8 @@ __global__ __launch_bounds__(D) void k_cache_read(CacheRowsArgs a, int nblk) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float v = (float)(e & 1 ? w[e >> 1].y : w[e >> 1].x);
-                    if constexpr (D == 128) y[e] = v * own + (float)(e & 1 ? o[e >> 1].y : o[e >> 1].x) * so;
+                    if constexpr (D == 128) y[e] = fmaf(v, own, (float)(e & 1 ? o[e >> 1].y : o[e >> 1].x) * so);
                     else y[e] = v * s;
-                    y[e] = flip(y[e], (sb >> e) & 1);
                 }
             } else {
                 const float s = sc[i][kv], c = -(float)off * s;          // exact: (u - off) s in one rounding
@@ -343,7 +360,7 @@ __global__ __launch_bounds__(D) void k_cache_read(CacheRowsArgs a, int nblk) {
             }
             if (on) {
                 const RowsView &dst = kv ? a.v : a.k;
-                store8(static_cast<T *>(dst.ptr) + ((int64_t)s0 + (t - f0)) * dst.ts + id.h * dst.hs + 8 * j, y);
+                store8(static_cast<T *>(dst.ptr) + ((int64_t)s0 + (t - f0)) * dst.ts + id.h * dst.hs + 8 * j, y, sb);
             }
         }
     }
