@@ -86,4 +86,38 @@ __device__ __forceinline__ float flip(float v, bool neg) { return neg ? -v : v; 
 // nibble of member e of a 4-bit unit
 __device__ __forceinline__ constexpr int nibble_of(int e) { return 4 * (e / 2 + 4 * (e % 2)); }
 
+// a unit of 8 codes as bf16 (4 bits: 128 + code, 8 bits: code)
+template <int BITS>
+__device__ __forceinline__ bf16x8 unit_bf16(const uint32_t *w) {
+    uint32_t r[4];
+    if constexpr (BITS == 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] = ((w[0] >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t v = w[i >> 1] >> (16 * (i & 1));
+            const uint32_t lo = __float_as_uint((float)(v & 255u)), hi = __float_as_uint((float)((v >> 8) & 255u));
+            r[i] = __builtin_amdgcn_perm(hi, lo, 0x07060302u);       // the upper halves: integers < 256 fit bf16
+        }
+    }
+    const uint4 q = make_uint4(r[0], r[1], r[2], r[3]);
+    return __builtin_bit_cast(bf16x8, q);
+}
+
+// N dwords from a 16-byte (N = 4, 8, ...) or 8-byte (N = 2) aligned address
+template <int N>
+__device__ __forceinline__ void load_dwords(const uint8_t *p, uint32_t (&w)[N]) {
+    if constexpr (N == 2) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        w[0] = v.x; w[1] = v.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(p + 4 * i);
+            w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
+        }
+    }
+}
+
 }  // namespace jolt

@@ -28,23 +28,24 @@ template <> __device__ __forceinline__ void load8<float>(const float *p, float (
     x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
     x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
 }
-// store 8 values, the sign of value e changed where bit e of `neg` is set
-template <typename T> __device__ __forceinline__ void store8(T *p, const float (&x)[8], uint32_t neg);
-template <> __device__ __forceinline__ void store8<uint16_t>(uint16_t *p, const float (&x)[8], uint32_t neg) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t two = neg >> (2 * i);
-        w[i] = bf16_pair(x[2 * i], x[2 * i + 1]) ^ (((two & 1u) << 15) | ((two & 2u) << 30));
-    }
-    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+// store 8 values, with the signs changed of those whose bit (15 or 31 of the
+// pair's word) is set
+template <typename T> __device__ __forceinline__ void store8_signed(T *p, const float (&x)[8], const uint32_t *neg);
+template <> __device__ __forceinline__ void store8_signed<uint16_t>(uint16_t *p, const float (&x)[8], const uint32_t *neg) {
+    *reinterpret_cast<uint4 *>(p) = make_uint4(bf16_pair(x[0], x[1]) ^ neg[0], bf16_pair(x[2], x[3]) ^ neg[1],
+                                               bf16_pair(x[4], x[5]) ^ neg[2], bf16_pair(x[6], x[7]) ^ neg[3]);
 }
-template <> __device__ __forceinline__ void store8<float>(float *p, const float (&x)[8], uint32_t neg) {
+template <> __device__ __forceinline__ void store8_signed<float>(float *p, const float (&x)[8], const uint32_t *neg) {
     float y[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(__float_as_uint(x[e]) ^ (((neg >> e) & 1u) << 31));
+    for (int e = 0; e < 8; ++e)
+        y[e] = __uint_as_float(__float_as_uint(x[e]) ^ ((e & 1) ? neg[e >> 1] & 0x80000000u : neg[e >> 1] << 16));
     reinterpret_cast<float4 *>(p)[0] = make_float4(y[0], y[1], y[2], y[3]);
     reinterpret_cast<float4 *>(p)[1] = make_float4(y[4], y[5], y[6], y[7]);
+}
+template <typename T> __device__ __forceinline__ void store8(T *p, const float (&x)[8]) {
+    constexpr uint32_t none[4] = {0, 0, 0, 0};
+    store8_signed(p, x, none);
 }
 
 // 8 codes as one unit: 8 bytes, or the 32-bit word of a 4-bit cache (in .x)
@@ -81,8 +82,6 @@ __device__ __forceinline__ uint2 member_mask(int e) {
     if constexpr (BITS == 4) return make_uint2(15u << nibble_of(e), 0);
     else return e < 4 ? make_uint2(255u << (8 * e), 0) : make_uint2(0, 255u << (8 * (e - 4)));
 }
-
-typedef short s16x2 __attribute__((ext_vector_type(2)));
 
 // Workgroups in the order of the dense rows: heads next to each other where a
 // token's heads are, token blocks where a head's tokens are.
@@ -212,31 +211,14 @@ __global__ __launch_bounds__(D) void k_cache_append(CacheRowsArgs a, int nblk) {
 }
 
 // ---------------------------------------------------------------- read
-// A thread (row r, lane j of D / 8) rebuilds features 8 j .. 8 j + 7 of one token
-// of a block of 8, and does so for kReadBlocks blocks at once, so that their
-// loads are in flight together.  The rotation of a group of 64 works on the
-// unsigned codes as packed 16-bit integers, two features to an instruction (at
-// most 64 * 255); their offset only reaches the group's feature 0, as 64 times
-// itself.  It is exact, so a value is s0 I0 +- s1 I1 with the scales times isd:
-// four roundings.
+// Rows stored as they are: a thread (row r, lane j of D / 8) rebuilds features
+// 8 j .. 8 j + 7 of one token of a block of 8, and does so for kReadBlocks blocks
+// at once, so that their loads are in flight together.
 constexpr int kReadBlocks = 2;
 
-// codes of features 8 j .. 8 j + 7 as 16-bit pairs (2 i, 2 i + 1)
+// member e of the units of 8 consecutive features, one a dword
 template <int BITS>
-__device__ __forceinline__ void key_codes(const uint8_t *codes, int64_t unit, s16x2 (&x)[4]) {
-    const uint2 w = load_unit<BITS>(codes, unit);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t u;
-        if constexpr (BITS == 4) u = (w.x >> (4 * i)) & 0x000F000Fu;
-        else u = __builtin_amdgcn_perm(0, i < 2 ? w.x : w.y, (i & 1) ? 0x0C030C02u : 0x0C010C00u);
-        x[i] = __builtin_bit_cast(s16x2, u);
-    }
-}
-// member e of the units of 8 consecutive features
-template <int BITS>
-__device__ __forceinline__ void value_codes(const uint8_t *codes, int64_t unit, int e, s16x2 (&x)[4]) {
-    uint32_t w[8];
+__device__ __forceinline__ void value_words(const uint8_t *codes, int64_t unit, int e, uint32_t (&w)[8]) {
     if constexpr (BITS == 4) {
         const uint4 *p = reinterpret_cast<const uint4 *>(codes + unit * 4);
         const uint4 a = p[0], b = p[1];
@@ -252,43 +234,11 @@ __device__ __forceinline__ void value_codes(const uint8_t *codes, int64_t unit, 
         }
     }
     const int sh = BITS == 4 ? nibble_of(e) : 8 * (e & 3);
-    constexpr uint32_t mask = BITS == 4 ? 15u : 255u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        x[i] = __builtin_bit_cast(s16x2, ((w[2 * i] >> sh) & mask) | (((w[2 * i + 1] >> sh) & mask) << 16));
-}
-template <int X>
-__device__ __forceinline__ s16x2 lane_xor_pair(s16x2 v) {
-    return __builtin_bit_cast(s16x2, __float_as_uint(lane_xor<X>(__uint_as_float(__builtin_bit_cast(uint32_t, v)))));
-}
-template <int X>
-__device__ __forceinline__ void fwht_pairs_lane(s16x2 (&x)[4], int j) {
-    const short s = (j & X) ? -1 : 1;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const s16x2 o = lane_xor_pair<X>(x[i]);
-        x[i] = x[i] * s16x2{s, s} + o;
-    }
-}
-// the 64-point transform over 8 lanes of 8 features each
-__device__ __forceinline__ void fwht_pairs(s16x2 (&x)[4], int j) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = s16x2{x[i].y, x[i].y} * s16x2{1, -1} + s16x2{x[i].x, x[i].x};
-#pragma unroll
-    for (int h = 1; h < 4; h *= 2)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (!(i & h)) {
-                const s16x2 a = x[i], b = x[i + h];
-                x[i] = a + b;
-                x[i + h] = a - b;
-            }
-    fwht_pairs_lane<1>(x, j);
-    fwht_pairs_lane<2>(x, j);
-    fwht_pairs_lane<4>(x, j);
+    for (int i = 0; i < 8; ++i) w[i] >>= sh;
 }
 
-template <typename T, int D, int BITS, bool ROT>
+template <typename T, int D, int BITS>
 __global__ __launch_bounds__(D) void k_cache_read(CacheRowsArgs a, int nblk) {
     const BlockId id = block_id(a, nblk);
     int s0;
@@ -301,9 +251,8 @@ __global__ __launch_bounds__(D) void k_cache_read(CacheRowsArgs a, int nblk) {
     const int tid = threadIdx.x, j = tid % (D / 8), r = tid / (D / 8);
     const int P = 1 << a.c.page_shift;
     const PageLayout pl = page_layout(P, D, BITS);
-    constexpr int off = 1 << (BITS - 1);
-    s16x2 x[kReadBlocks][2][4];
-    float sc[kReadBlocks][2];
+    constexpr float off = (float)(1 << (BITS - 1));
+    float x[kReadBlocks][2][8], sc[kReadBlocks][2];
 #pragma unroll
     for (int i = 0; i < kReadBlocks; ++i) {
         const int64_t t = tok8 + 8 * i;
@@ -315,52 +264,184 @@ __global__ __launch_bounds__(D) void k_cache_read(CacheRowsArgs a, int nblk) {
         for (int kv = 0; kv < 2; ++kv) {
             sc[i][kv] = 0.f;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[i][kv][e] = s16x2{off, off};
+            for (int e = 0; e < 8; ++e) x[i][kv][e] = 0.f;
             if (have)
                 sc[i][kv] = bf16_to_f32(reinterpret_cast<const uint16_t *>(base + (kv ? pl.v_scales : pl.k_scales))[(j >> 3) * P + tin + r]);
         }
         if (have) {
-            key_codes<BITS>(base, (int64_t)(tin + r) * (D / 8) + (j & 3) * (D / 32) + (j >> 2), x[i][0]);
-            value_codes<BITS>(base + pl.v_codes, (int64_t)(tin >> 3) * D + 8 * j, r, x[i][1]);
+            const uint2 k = load_unit<BITS>(base, (int64_t)(tin + r) * (D / 8) + (j & 3) * (D / 32) + (j >> 2));
+            uint32_t v[8];
+            value_words<BITS>(base + pl.v_codes, (int64_t)(tin >> 3) * D + 8 * j, r, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                x[i][0][e] = (float)unit_code<BITS>(k, e);
+                x[i][1][e] = (float)(v[e] & (BITS == 4 ? 15u : 255u));
+            }
         }
     }
 #pragma unroll
     for (int i = 0; i < kReadBlocks; ++i) {
         const int64_t t = tok8 + 8 * i + r;
-        const bool on = t >= f0 && t < f0 + n;
+        if (t < f0 || t >= f0 + n) continue;
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
-            s16x2(&w)[4] = x[i][kv];
+            const float s = sc[i][kv], c = -off * s;         // exact: (u - off) s in one rounding
             float y[8];
-            uint32_t sb = 0;
-            if constexpr (ROT) {
-                fwht_pairs(w, j);
-                if ((j & 7) == 0) w[0].x -= 64 * off;
-                const float s = sc[i][kv] * (D == 128 ? 0.08838834764831845f : 0.125f);
-                sb = sign_byte(kv ? a.c.sv : a.c.sk, j);
-                s16x2 o[4];
-                float so = 0.f;
-                if constexpr (D == 128) {
-                    // feature f + 64 of the row is I0 - I1 where f is I0 + I1
-                    so = lane_xor<8>(s);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) o[e] = lane_xor_pair<8>(w[e]);
+            for (int e = 0; e < 8; ++e) y[e] = fmaf(x[i][kv][e], s, c);
+            const RowsView &dst = kv ? a.v : a.k;
+            store8(static_cast<T *>(dst.ptr) + ((int64_t)s0 + (t - f0)) * dst.ts + id.h * dst.hs + 8 * j, y);
+        }
+    }
+}
+
+// Rotated rows: H is symmetric and its own inverse up to d, and the transform of
+// a group of 64 integer codes is a matrix product with the +-1 matrix H64, exact
+// in bf16 operands and fp32 sums (at most 64 * 255).  One wave takes 64 tokens of
+// a head, 16 at a time: products 16x16x32 with A = H64 (rows = features) and B =
+// the codes (columns = tokens), the offset of the codes in the initial value of
+// feature 0, the only one it reaches.  Rows of A are ordered so that a lane (token
+// m, part g) ends with features 8 g .. 8 g + 7 and 32 on from them of each group,
+// and four lanes store 64 bytes side by side.  Then
+//   y_f = isd (s0 I0 + s1 I1),  y_(f+64) = isd (s0 I0 - s1 I1)   (d = 128)
+// with the scales times isd: four roundings.  On the vector unit the butterflies
+// cost five times the instructions and bound the kernel (202 us for 16 tails of
+// 8192 tokens of 8 heads against 134 us of memory traffic).
+template <typename T, int D, int BITS>
+__global__ __launch_bounds__(64, 3) void k_cache_read_rot(CacheRowsArgs a, int nblk) {
+    constexpr int NG = D / 64, kTok = 64;
+    const BlockId id = block_id(a, nblk);
+    int s0;
+    const int n = min(ragged_rows(a.starts, id.b, a.total, &s0), a.max_rows);
+    if (n == 0) return;
+    const int64_t f0 = a.first ? a.first[id.b] : 0;
+    const int64_t tok = (f0 >> 4) * 16 + (int64_t)id.blk * kTok;
+    if (tok >= f0 + n) return;
+    const int len = cache_len(a.c, id.b);
+    const int lane = threadIdx.x, m = lane & 15, g = lane >> 4;
+    const int P = 1 << a.c.page_shift;
+    const PageLayout pl = page_layout(P, D, BITS);
+
+    // H64 fragments: row m of tile t is feature f = 32 (t / 2) + 8 (m / 4) + 4 (t % 2) +
+    // m % 4; the lane holds columns 32 k + 8 g + e: the signs over e from f's low bits, the rest for all
+    bf16x8 hf[4][2];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        const uint32_t f = 32 * (t >> 1) + 8 * (m >> 2) + 4 * (t & 1) + (m & 3);
+        uint32_t r[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t p = __popc(f & (2 * i)) & 1;      // element 2 i; 2 i + 1 has f's lowest bit on top
+            r[i] = 0x3F803F80u ^ (p << 15) ^ ((p ^ (f & 1)) << 31);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const uint32_t all = (__popc((f >> 3) & (4 * k + g)) & 1) ? 0x80008000u : 0u;
+            hf[t][k] = __builtin_bit_cast(bf16x8, make_uint4(r[0] ^ all, r[1] ^ all, r[2] ^ all, r[3] ^ all));
+        }
+    }
+    // all of the 64 tokens' codes and scales are under way before the first is used;
+    // V's go through LDS, from where a lane takes its token's member of 8 units
+    constexpr int kBlk = kTok / 16, KU = BITS / 4, KN = D / 32 * KU, VN = D * BITS / 128;
+    __shared__ __align__(16) uint32_t vlds[kBlk][VN * 64];
+    uint32_t kw[kBlk][KN], vw[kBlk][VN];
+    uint16_t sraw[kBlk][2][NG];
+#pragma unroll
+    for (int blk = 0; blk < kBlk; ++blk) {
+        const int64_t t16 = tok + 16 * blk;
+        const int page = t16 >= 0 && t16 < len && t16 < f0 + n ? cache_page(a.c, id.b, (int)t16) : -1;
+#pragma unroll
+        for (int i = 0; i < KN; ++i) kw[blk][i] = 0;
+#pragma unroll
+        for (int i = 0; i < VN; ++i) vw[blk][i] = 0;
+#pragma unroll
+        for (int q = 0; q < NG; ++q) sraw[blk][0][q] = sraw[blk][1][q] = 0;
+        if (page >= 0) {
+            const uint8_t *base = a.c.pool + cache_block_offset(a.c, page, id.h);
+            const int tin = (int)(t16 & (P - 1));
+            load_dwords<KN>(base + (tin + m) * (D * BITS / 8) + g * (KN * 4), kw[blk]);
+            load_dwords<VN>(base + pl.v_codes + (tin >> 3) * (D * BITS) + lane * (VN * 4), vw[blk]);
+            if (t16 + m < len)
+#pragma unroll
+                for (int q = 0; q < NG; ++q) {
+                    sraw[blk][0][q] = reinterpret_cast<const uint16_t *>(base + pl.k_scales)[q * P + tin + m];
+                    sraw[blk][1][q] = reinterpret_cast<const uint16_t *>(base + pl.v_scales)[q * P + tin + m];
                 }
-                const float own = (j & 8) ? -s : s;
+        }
+    }
+#pragma unroll
+    for (int blk = 0; blk < kBlk; ++blk)
+#pragma unroll
+        for (int i = 0; i < VN; ++i) vlds[blk][lane * VN + i] = vw[blk][i];
+    __syncthreads();
+    const float isd = D == 128 ? 0.08838834764831845f : 0.125f;
+    const float start = g == 0 ? -64.f * (BITS == 4 ? 136.f : 128.f) : 0.f;
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+        // this lane's output signs, two features to a word, at bits 15 and 31
+        uint32_t neg[NG][8];
+#pragma unroll
+        for (int q = 0; q < NG; ++q) {
+            const uint32_t(&sb)[4] = kv ? a.c.sv : a.c.sk;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t w = sb[2 * q + (i >> 2)] >> (8 * g + 2 * (i & 3));
+                neg[q][i] = ((w & 1u) << 15) | ((w & 2u) << 30);
+            }
+        }
+        const RowsView &dst = kv ? a.v : a.k;
+#pragma unroll
+        for (int blk = 0; blk < kBlk; ++blk) {
+            const int64_t t = tok + 16 * blk + m;
+            if (tok + 16 * blk >= f0 + n) break;
+            float sc[NG];
+            bf16x8 cf[D / 32];
+#pragma unroll
+            for (int q = 0; q < NG; ++q) sc[q] = bf16_to_f32(sraw[blk][kv][q]);
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+                if (kv == 0) cf[k] = unit_bf16<BITS>(&kw[blk][k * KU]);
+                else {
+                    uint32_t w[8], r[4];
+                    value_words<BITS>(reinterpret_cast<const uint8_t *>(vlds[blk]), (m >> 3) * D + 32 * k + 8 * g, m & 7, w);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if constexpr (BITS == 4)
+                            r[i] = (__builtin_amdgcn_perm(w[2 * i + 1], w[2 * i], 0x0C040C00u) & 0x000F000Fu) | 0x43004300u;
+                        else
+                            r[i] = __builtin_amdgcn_perm(__float_as_uint((float)(w[2 * i + 1] & 255u)),
+                                                         __float_as_uint((float)(w[2 * i] & 255u)), 0x07060302u);
+                    }
+                    cf[k] = __builtin_bit_cast(bf16x8, make_uint4(r[0], r[1], r[2], r[3]));
+                }
+            }
+            f32x4 x[NG][4];
+#pragma unroll
+            for (int q = 0; q < NG; ++q)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[q][i] = f32x4{i == 0 ? start : 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        x[q][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hf[i][k], cf[2 * q + k], x[q][i], 0, 0, 0);
+                }
+            if (t < f0 || t >= f0 + n) continue;
+            T *row = static_cast<T *>(dst.ptr) + ((int64_t)s0 + (t - f0)) * dst.ts + id.h * dst.hs + 8 * g;
+            const float sa = sc[0] * isd, sb = NG == 2 ? sc[NG - 1] * isd : 0.f;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                float lo[8], hi[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float v = (float)(e & 1 ? w[e >> 1].y : w[e >> 1].x);
-                    if constexpr (D == 128) y[e] = fmaf(v, own, (float)(e & 1 ? o[e >> 1].y : o[e >> 1].x) * so);
-                    else y[e] = v * s;
+                    const int i = 2 * half + (e >> 2), y = e & 3;
+                    lo[e] = x[0][i][y] * sa;
+                    if constexpr (NG == 2) {
+                        hi[e] = fmaf(x[NG - 1][i][y], -sb, lo[e]);
+                        lo[e] = fmaf(x[NG - 1][i][y], sb, lo[e]);
+                    }
                 }
-            } else {
-                const float s = sc[i][kv], c = -(float)off * s;          // exact: (u - off) s in one rounding
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = fmaf((float)(e & 1 ? w[e >> 1].y : w[e >> 1].x), s, c);
-            }
-            if (on) {
-                const RowsView &dst = kv ? a.v : a.k;
-                store8(static_cast<T *>(dst.ptr) + ((int64_t)s0 + (t - f0)) * dst.ts + id.h * dst.hs + 8 * j, y, sb);
+                store8_signed(row + 32 * half, lo, &neg[0][4 * half]);
+                if constexpr (NG == 2) store8_signed(row + 64 + 32 * half, hi, &neg[NG - 1][4 * half]);
             }
         }
     }
@@ -447,16 +528,21 @@ __global__ __launch_bounds__(256) void k_cache_keep(CacheKeepArgs a) {
 }
 
 // ---------------------------------------------------------------- launchers
-// blocks of 8 tokens that at most n consecutive tokens touch
-static int64_t blocks8(int n) { return ((int64_t)n + 6) / 8 + 1; }
+// aligned blocks of `size` tokens that at most n consecutive tokens touch
+static int64_t blocks_of(int size, int n) { return ((int64_t)n + size - 2) / size + 1; }
 
 template <typename T, int D, int BITS, bool ROT>
 static hipError_t rows_launch(const CacheRowsArgs &a, bool read, hipStream_t s) {
-    const int64_t b8 = blocks8(a.max_rows), nblk = read ? (b8 + kReadBlocks - 1) / kReadBlocks : b8;
+    // a rotated read's blocks of 64 tokens begin at a multiple of 16
+    const int64_t nblk = !read ? blocks_of(8, a.max_rows)
+                               : (ROT ? (16 * blocks_of(16, a.max_rows) + 63) / 64
+                                      : (blocks_of(8, a.max_rows) + kReadBlocks - 1) / kReadBlocks);
     const int64_t grid = nblk * a.c.H * a.c.batch;
     if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
-    if (read) hipLaunchKernelGGL((k_cache_read<T, D, BITS, ROT>), dim3((unsigned)grid), dim3(D), 0, s, a, (int)nblk);
-    else hipLaunchKernelGGL((k_cache_append<T, D, BITS, ROT>), dim3((unsigned)grid), dim3(D), 0, s, a, (int)nblk);
+    const dim3 g((unsigned)grid);
+    if (!read) hipLaunchKernelGGL((k_cache_append<T, D, BITS, ROT>), g, dim3(D), 0, s, a, (int)nblk);
+    else if constexpr (ROT) hipLaunchKernelGGL((k_cache_read_rot<T, D, BITS>), g, dim3(64), 0, s, a, (int)nblk);
+    else hipLaunchKernelGGL((k_cache_read<T, D, BITS>), g, dim3(D), 0, s, a, (int)nblk);
     return hipGetLastError();
 }
 template <typename T, int D, int BITS>

@@ -35,40 +35,8 @@ __device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-// a unit of 8 codes as bf16 (4 bits: 128 + code, 8 bits: code)
-template <int BITS>
-__device__ __forceinline__ bf16x8 unit_bf16(const uint32_t *w) {
-    uint32_t r[4];
-    if constexpr (BITS == 4) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) r[i] = ((w[0] >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t v = w[i >> 1] >> (16 * (i & 1));
-            const uint32_t lo = __float_as_uint((float)(v & 255u)), hi = __float_as_uint((float)((v >> 8) & 255u));
-            r[i] = __builtin_amdgcn_perm(hi, lo, 0x07060302u);       // the upper halves: integers < 256 fit bf16
-        }
-    }
-    const uint4 q = make_uint4(r[0], r[1], r[2], r[3]);
-    return __builtin_bit_cast(bf16x8, q);
-}
 template <int BITS> constexpr float code_offset() { return BITS == 4 ? 136.f : 128.f; }
 
-// N dwords from a 16-byte (N = 4, 8, ...) or 8-byte (N = 2) aligned address
-template <int N>
-__device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[N]) {
-    if constexpr (N == 2) {
-        const uint2 v = *reinterpret_cast<const uint2 *>(p);
-        w[0] = v.x; w[1] = v.y;
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; i += 4) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(p + 4 * i);
-            w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
-        }
-    }
-}
 __device__ __forceinline__ float scale_of(const uint32_t *w, int e) {
     return __uint_as_float((e & 1) ? (w[e >> 1] & 0xFFFF0000u) : (w[e >> 1] << 16));
 }
@@ -88,19 +56,19 @@ struct BlockRegs {
         constexpr int rowb = D * BITS / 8;
 #pragma unroll
         for (int u = 0; u < 2; ++u)
-            load_words<kK>(blk + (tin + 8 * (m >> 2) + 4 * u + (m & 3)) * rowb + g * (rowb / 4), k[u]);
+            load_dwords<kK>(blk + (tin + 8 * (m >> 2) + 4 * u + (m & 3)) * rowb + g * (rowb / 4), k[u]);
         const uint8_t *vp = blk + pl.v_codes + ((tin >> 3) + g) * (D * BITS);
 #pragma unroll
         for (int i = 0; i < kV; i += 4) {
             uint32_t t[4];
-            load_words<4>(vp + i * 64 + m * 16, t);     // 16 lanes x 16 bytes per step
+            load_dwords<4>(vp + i * 64 + m * 16, t);     // 16 lanes x 16 bytes per step
 #pragma unroll
             for (int x = 0; x < 4; ++x) v[i + x] = t[x];
         }
 #pragma unroll
         for (int q = 0; q < D / 64; ++q) {
-            load_words<4>(blk + pl.k_scales + (q * P + tin + 8 * g) * 2, ks[q]);
-            load_words<4>(blk + pl.v_scales + (q * P + tin + 8 * g) * 2, vs[q]);
+            load_dwords<4>(blk + pl.k_scales + (q * P + tin + 8 * g) * 2, ks[q]);
+            load_dwords<4>(blk + pl.v_scales + (q * P + tin + 8 * g) * 2, vs[q]);
         }
     }
 };
