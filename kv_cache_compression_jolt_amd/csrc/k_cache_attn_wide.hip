@@ -578,7 +578,10 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
                         uint32_t vis = col.sees8(tree, base, t0 + 32 * u + 16 * x + 8 * hh);
                         if ((u ? cur.p1 : cur.p0) < 0) vis = 0;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) s[u][8 * x + e] = (vis >> e) & 1 ? s[u][8 * x + e] : neg_inf();
+                        for (int e = 0; e < 8; ++e) {         // all ones or zeros from the bit picks the score or -inf
+                            const uint32_t keep = (uint32_t)__builtin_amdgcn_sbfe((int)vis, e, 1);
+                            s[u][8 * x + e] = __uint_as_float((__float_as_uint(s[u][8 * x + e]) & keep) | (~keep & 0xFF800000u));
+                        }
                     }
             }
             float mx = s[0][0];
