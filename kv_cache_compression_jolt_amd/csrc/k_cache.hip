@@ -160,16 +160,13 @@ __global__ __launch_bounds__(D) void k_cache_append(CacheRowsArgs a, int nblk) {
     if (last < from) return;
     const int tok8 = ((from >> 3) + id.blk) * 8;
     if (tok8 > last) return;
-    const int page = cache_page(a.c, id.b, tok8);
-    if (page < 0) return;
-    uint8_t *base = a.c.pool + cache_block_offset(a.c, page, id.h);
-    const int P = 1 << a.c.page_shift, tin = tok8 & (P - 1);
-    const PageLayout pl = page_layout(P, D, BITS);
     const int tid = threadIdx.x, j = tid % (D / 8), r = tid / (D / 8), t = tok8 + r;
     const bool on = t >= from && t <= last;
     const int64_t row = (int64_t)s0 + (t - t0);
     __shared__ __align__(16) uint8_t vc[8][D];
-    float in[2][8];                                      // both rows are under way before either is used
+    // both rows, and the V units that the block keeps other tokens in, are under
+    // way before any is used
+    float in[2][8];
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
         const RowsView &src = kv ? a.v : a.k;
@@ -177,6 +174,14 @@ __global__ __launch_bounds__(D) void k_cache_append(CacheRowsArgs a, int nblk) {
         for (int e = 0; e < 8; ++e) in[kv][e] = 0.f;
         if (on) load8(static_cast<const T *>(src.ptr) + row * src.ts + id.h * src.hs + 8 * j, in[kv]);
     }
+    const int page = cache_page(a.c, id.b, tok8);
+    if (page < 0) return;
+    uint8_t *base = a.c.pool + cache_block_offset(a.c, page, id.h);
+    const int P = 1 << a.c.page_shift, tin = tok8 & (P - 1);
+    const PageLayout pl = page_layout(P, D, BITS);
+    const int64_t unit = (int64_t)(tin >> 3) * D + tid;
+    const bool part = tok8 < from || tok8 + 7 > last;
+    const uint2 old = part ? load_unit<BITS>(base + pl.v_codes, unit) : make_uint2(0, 0);
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
         float(&x)[8] = in[kv];
@@ -205,8 +210,7 @@ __global__ __launch_bounds__(D) void k_cache_append(CacheRowsArgs a, int nblk) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) u[e] = vc[e][tid];
     uint2 w = pack_unit<BITS>(u);
-    const int64_t unit = (int64_t)(tin >> 3) * D + tid;
-    if (tok8 < from || tok8 + 7 > last) {
+    if (part) {
         uint2 m = make_uint2(0, 0);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -215,9 +219,8 @@ __global__ __launch_bounds__(D) void k_cache_append(CacheRowsArgs a, int nblk) {
                 m.x |= me.x;
                 m.y |= me.y;
             }
-        const uint2 o = load_unit<BITS>(base + pl.v_codes, unit);
-        w.x = (w.x & m.x) | (o.x & ~m.x);
-        w.y = (w.y & m.y) | (o.y & ~m.y);
+        w.x = (w.x & m.x) | (old.x & ~m.x);
+        w.y = (w.y & m.y) | (old.y & ~m.y);
     }
     store_unit<BITS>(base + pl.v_codes, unit, w);
 }
