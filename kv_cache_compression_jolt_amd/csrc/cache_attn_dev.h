@@ -140,6 +140,39 @@ struct Reach {
     }
 };
 
+// The last steps of a row: its log-sum-exp and the weights of its own sums and of
+// the part to be merged in.
+struct RowEnd {
+    float own, other, lse;
+};
+__device__ __forceinline__ RowEnd row_end(const CacheAttnArgs &a, int64_t at, float m, float l) {
+    RowEnd r{1.f, 0.f, l == 0.f ? neg_inf() : (m + __builtin_amdgcn_logf(l)) * kLn2};
+    if (a.merge_out) {
+        const float l2 = a.merge_lse[at], mx = fmaxf(r.lse, l2);
+        const float w1 = mx == neg_inf() ? 0.f : __builtin_amdgcn_exp2f((r.lse - mx) * kLog2e);
+        const float w2 = mx == neg_inf() ? 0.f : __builtin_amdgcn_exp2f((l2 - mx) * kLog2e);
+        const float s = w1 + w2, is = s == 0.f ? 0.f : 1.f / s;
+        r.own = w1 * is;
+        r.other = w2 * is;
+        r.lse = s == 0.f ? neg_inf() : mx + __builtin_amdgcn_logf(s) * kLn2;
+    }
+    return r;
+}
+// 8 features from f on; a part that saw nothing adds nothing, whatever its rows hold
+template <int D>
+__device__ __forceinline__ void store_out8(const CacheAttnArgs &a, int64_t row, int head, int f, float (&o)[8], const RowEnd &r) {
+    if (a.merge_out) {
+        const float4 *p = reinterpret_cast<const float4 *>(a.merge_out + (row * a.hq + head) * D + f);
+        const float4 x = p[0], y = p[1];
+        const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = (r.own == 0.f ? 0.f : o[e] * r.own) + (r.other == 0.f ? 0.f : v[e] * r.other);
+    }
+    uint16_t *dst = static_cast<uint16_t *>(a.out.ptr) + row * a.out.ts + head * a.out.hs + f;
+    *reinterpret_cast<uint4 *>(dst) =
+        make_uint4(bf16_pair(o[0], o[1]), bf16_pair(o[2], o[3]), bf16_pair(o[4], o[5]), bf16_pair(o[6], o[7]));
+}
+
 // out row: o (8 features of lane j of D/8), l and m (log2 domain) of the whole row
 template <int D, bool ROT>
 __device__ __forceinline__ void finish_row(const CacheAttnArgs &a, int64_t row, int head, int j, float (&o)[8], float m,
@@ -155,27 +188,10 @@ __device__ __forceinline__ void finish_row(const CacheAttnArgs &a, int64_t row, 
         for (int e = 0; e < 8; ++e) o[e] = flip(o[e] * isd, (sb >> e) & 1);
     }
     if (!store) return;
-    float lse = l == 0.f ? neg_inf() : (m + __builtin_amdgcn_logf(l)) * kLn2;
     const int64_t at = row * a.hq + head;
-    if (a.merge_out) {
-        const float l2 = a.merge_lse[at], mx = fmaxf(lse, l2);
-        const float w1 = mx == neg_inf() ? 0.f : __builtin_amdgcn_exp2f((lse - mx) * kLog2e);
-        const float w2 = mx == neg_inf() ? 0.f : __builtin_amdgcn_exp2f((l2 - mx) * kLog2e);
-        const float s = w1 + w2, is = s == 0.f ? 0.f : 1.f / s;
-        const float4 *p = reinterpret_cast<const float4 *>(a.merge_out + at * D + 8 * j);
-        const float4 x = p[0], y = p[1];
-        const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {                   // a part that saw nothing adds nothing, whatever its rows hold
-            const float p1 = w1 == 0.f ? 0.f : o[e] * w1, p2 = w2 == 0.f ? 0.f : v[e] * w2;
-            o[e] = (p1 + p2) * is;
-        }
-        lse = s == 0.f ? neg_inf() : mx + __builtin_amdgcn_logf(s) * kLn2;
-    }
-    uint16_t *dst = static_cast<uint16_t *>(a.out.ptr) + row * a.out.ts + head * a.out.hs + 8 * j;
-    *reinterpret_cast<uint4 *>(dst) =
-        make_uint4(bf16_pair(o[0], o[1]), bf16_pair(o[2], o[3]), bf16_pair(o[4], o[5]), bf16_pair(o[6], o[7]));
-    if (a.lse && j == 0) a.lse[at] = lse;
+    const RowEnd r = row_end(a, at, m, l);
+    store_out8<D>(a, row, head, 8 * j, o, r);
+    if (a.lse && j == 0) a.lse[at] = r.lse;
 }
 
 }  // namespace jolt

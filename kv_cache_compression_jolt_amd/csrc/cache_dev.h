@@ -48,11 +48,12 @@ __device__ __forceinline__ uint32_t group_umax(uint32_t v) {
 
 template <int X, typename T>
 __device__ __forceinline__ void fwht_lanes(T (&x)[8], int j) {
-    const bool up = j & X;
+    const T s = (j & X) ? T(-1) : T(1);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const T o = lane_xor<X>(x[e]);
-        x[e] = up ? o - x[e] : x[e] + o;
+        if constexpr (sizeof(T) == 8) x[e] = fma(x[e], s, o);      // o + x or o - x, rounded once
+        else x[e] = fmaf(x[e], s, o);
     }
 }
 // Unscaled Sylvester Hadamard transform of rows of D features, lane j of the

@@ -81,6 +81,22 @@ __device__ __forceinline__ uint32_t dpp_u(uint32_t v) {
     return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, Ctrl, 0xF, 0xF, false);
 }
 
+// two +-1 in bf16: the signs of H at (f, c) and (f, c + 1), c even
+__device__ __forceinline__ uint32_t sign_ones(uint32_t f, uint32_t c) {
+    const uint32_t p = __popc(f & c) & 1;
+    return 0x3F803F80u ^ (p << 15) ^ ((p ^ (f & 1)) << 31);
+}
+// the fragment with these signs over its elements and parity(f & c) for all
+__device__ __forceinline__ bf16x8 sign_frag(const uint32_t (&b)[4], uint32_t f, uint32_t c) {
+    const uint32_t all = (__popc(f & c) & 1) ? 0x80008000u : 0u;
+    return __builtin_bit_cast(bf16x8, make_uint4(b[0] ^ all, b[1] ^ all, b[2] ^ all, b[3] ^ all));
+}
+// bits e and e + 1 of s as the signs of a bf16 pair
+__device__ __forceinline__ uint32_t sign_pair(uint32_t s, int e) {
+    const uint32_t two = s >> e;
+    return ((two & 1u) << 15) | ((two & 2u) << 30);
+}
+
 // One thread's share of a tile: UPT units of K and of V and the scales they
 // need; all: two scales a lane of each half of the tile (lanes 0..31 K, 32..63
 // V), for the tile's largest.
@@ -104,9 +120,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
     constexpr int kKBytes = D / 8 * kKStride, kVBytes = kTile / 8 * D * 16;
     constexpr int kSBytes = kPost ? NG * kTile * 4 : 0;
     constexpr int kVBuf = kVBytes + kSBytes;           // the K scales of 8-bit codes lie behind V
-    constexpr int kOutCols = 16;                       // columns of a wave that leave through LDS together
-    constexpr int kOut = NW * kOutCols * (D + 4) * 4;
-    constexpr int kMain = 2 * kKBytes + 3 * kVBuf > kOut ? 2 * kKBytes + 3 * kVBuf : kOut;
+    constexpr int kMain = 2 * kKBytes + 3 * kVBuf;
     constexpr bool kLo = ROT;                          // the queries' second parts stay in LDS: a lane's own fragments
     __shared__ __align__(16) uint8_t lds[kMain + (kLo ? NW * NK * 1024 : 0)];
     uint8_t *const qlo = lds + kMain + (threadIdx.x >> 6) * (NK * 1024) + (threadIdx.x & 63) * 16;
@@ -128,69 +142,78 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
     const int c0 = (ct * NW + wave) * 32;              // this wave's columns
     const bool active = c0 < ncol;
 
-    // ---- queries: 16 columns of the wave at a time through its part of LDS
+    // token (feature) of row m of a product: bits 2 and 3 exchanged, so that a lane's
+    // results j = 8 t + i are tokens (features) 16 t + 8 hh + i: two operands of a
+    // following product, or two pieces of 8 in memory
+    const int mtok = (m & 19) | ((m & 4) << 1) | ((m & 8) >> 1);
+
+    // ---- queries: lane (column m, half hh) has features 16 k + 8 hh + e of its row
     f16x8 qf[NK];
     float qmul = 0.f;                                  // what the column's scores are multiplied with
     {
-        float *sq = reinterpret_cast<float *>(lds) + wave * kOutCols * (D + 4);
-        constexpr int RL = D / 8, RW = 64 / RL;        // lanes of a row, rows of a pass
-        const int r = lane / RL, j = lane % RL;
+        const int c = c0 + m;
+        float x[NF][16];                               // features 32 i + 16 t + 8 hh + e at [i][8 t + e]
+        uint4 q[NK];
+        {
+            const int cq = c < ncol ? c : c0 < ncol ? ncol - 1 : 0;      // (a column past the last repeats one)
+            const uint16_t *row = static_cast<const uint16_t *>(a.q.ptr) + (int64_t)(s0 + cq / a.G) * a.q.ts +
+                                  (h * a.G + cq % a.G) * a.q.hs + 8 * hh;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
+            for (int k = 0; k < NK; ++k) q[k] = *reinterpret_cast<const uint4 *>(row + 16 * k);
+        }
+        if constexpr (ROT) {
+            // H (s o q) as a product with the +-1 matrix: exact bf16 operands, fp32 sums
 #pragma unroll
-            for (int it = 0; it < kOutCols / RW; ++it) {
-                const int cc = it * RW + r, c = c0 + half * 16 + cc;
-                float x[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = 0.f;
-                if (c < ncol) {
-                    const int i = c / a.G, hd = h * a.G + c % a.G;
-                    const uint4 v = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q.ptr) +
-                                                                     (int64_t)(s0 + i) * a.q.ts + hd * a.q.hs + 8 * j);
-                    const uint32_t q[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = __uint_as_float((e & 1) ? (q[e >> 1] & 0xFFFF0000u) : (q[e >> 1] << 16));
-                }
-                if constexpr (ROT) {
-                    const uint32_t sb = sign_byte(a.c.sk, j);
-                    const float isd = D == 128 ? 0.08838834764831845f : 0.125f;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = flip(x[e], (sb >> e) & 1);
-                    fwht_row<D>(x, j);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] *= isd;
-                }
-                uint32_t am = 0;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) am = max(am, __float_as_uint(x[e]) & 0x7FFFFFFFu);
-                am = group_umax<RL>(am);
-                // 2^-e brings the largest feature to [1, 2); its inverse goes into qmul
-                const int ex = min(max((int)(am >> 23), 1), 253);
-                const float down = __uint_as_float((uint32_t)(254 - ex) << 23), up = __uint_as_float((uint32_t)ex << 23);
-                float4 *p = reinterpret_cast<float4 *>(sq + cc * (D + 4) + 8 * j);
-                p[0] = make_float4(x[0] * down, x[1] * down, x[2] * down, x[3] * down);
-                p[1] = make_float4(x[4] * down, x[5] * down, x[6] * down, x[7] * down);
-                if (j == 0) sq[cc * (D + 4) + D] = up;
+            for (int k = 0; k < NK; ++k) {
+                const uint32_t sb = sign_byte(a.c.sk, 2 * k + hh);
+                q[k].x ^= sign_pair(sb, 0);
+                q[k].y ^= sign_pair(sb, 2);
+                q[k].z ^= sign_pair(sb, 4);
+                q[k].w ^= sign_pair(sb, 6);
             }
-            wave_lds_sync();
-            if ((m >> 4) == half) {
-                const float *row = sq + (m & 15) * (D + 4);
-                qmul = row[D];
 #pragma unroll
-                for (int k = 0; k < NK; ++k) {
-                    const float *p = row + 16 * k + 8 * hh;
-                    uint32_t hi[4], lo[4];
+            for (int i = 0; i < NF; ++i) {
+                const uint32_t f = 32 * i + mtok;
+                f32x16 y{};
+                uint32_t b[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float x0 = p[2 * i], x1 = p[2 * i + 1];
-                        hi[i] = f16_pair(x0, x1);
-                        lo[i] = f16_pair(x0 - (float)h2(hi[i])[0], x1 - (float)h2(hi[i])[1]);
-                    }
-                    qf[k] = __builtin_bit_cast(f16x8, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-                    if constexpr (kLo) *reinterpret_cast<uint4 *>(qlo + k * 1024) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                }
+                for (int r = 0; r < 4; ++r) b[r] = sign_ones(f, 2 * r);
+#pragma unroll
+                for (int k = 0; k < NK; ++k)
+                    y = __builtin_amdgcn_mfma_f32_32x32x16_bf16(sign_frag(b, f, 16 * k + 8 * hh), __builtin_bit_cast(bf16x8, q[k]), y, 0, 0, 0);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[i][e] = y[e];
             }
-            wave_lds_sync();
+        } else {
+#pragma unroll
+            for (int k = 0; k < NK; ++k) {
+                const uint32_t w[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    x[k / 2][8 * (k & 1) + e] = __uint_as_float((e & 1) ? (w[e >> 1] & 0xFFFF0000u) : (w[e >> 1] << 16));
+            }
+        }
+        // 2^-ex brings the row's largest feature to [1, 2); its inverse goes into qmul
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < NF; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(x[i][e]));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const int ex = min(max((int)(__float_as_uint(top) >> 23), 1), 253);
+        const float down = __uint_as_float((uint32_t)(254 - ex) << 23);
+        qmul = __uint_as_float((uint32_t)ex << 23) * (!ROT ? 1.f : D == 128 ? 0.08838834764831845f : 0.125f);
+#pragma unroll
+        for (int k = 0; k < NK; ++k) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float x0 = x[k / 2][8 * (k & 1) + 2 * i] * down, x1 = x[k / 2][8 * (k & 1) + 2 * i + 1] * down;
+                hi[i] = f16_pair(x0, x1);
+                if constexpr (kLo) lo[i] = f16_pair(x0 - (float)h2(hi[i])[0], x1 - (float)h2(hi[i])[1]);
+            }
+            qf[k] = __builtin_bit_cast(f16x8, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+            if constexpr (kLo) *reinterpret_cast<uint4 *>(qlo + k * 1024) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
     }
 
@@ -399,8 +422,6 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
         return ek;
     };
 
-    // token of K row m: bits 2 and 3 exchanged, so that a lane's scores are 8 consecutive tokens twice
-    const int mtok = (m & 19) | ((m & 4) << 1) | ((m & 8) >> 1);
     uint8_t *const vlds = lds + 2 * kKBytes;
 
     // Two groups of waves, one on each half of every SIMD's slots, take turns at
@@ -636,51 +657,88 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
     }
     __syncthreads();
 
-    // ---- rows out, 16 columns of the wave at a time
+    // ---- rows out: lane (column m, half hh) has features 32 i + 8 (j / 4) + 4 hh + j % 4
     if (!active) return;
     lrun += __shfl_xor(lrun, 32);
     const float vunit = __builtin_ldexpf(1.f, erun - 127 - (kTop - 15));
-    float *so = reinterpret_cast<float *>(lds) + wave * kOutCols * (D + 4);
-    constexpr int RL = D / 8, RW = 64 / RL;
-    const int r = lane / RL, j = lane % RL;
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        if ((m >> 4) == half) {
-            float *row = so + (m & 15) * (D + 4);
-#pragma unroll
-            for (int i = 0; i < NF; ++i)
-#pragma unroll
-                for (int x = 0; x < 16; ++x) row[32 * i + 8 * (x >> 2) + 4 * hh + (x & 3)] = acc[i][x] * vunit;
-            if (hh == 0) {
-                row[D] = mrun;
-                row[D + 1] = lrun;
-            }
+    const int64_t qrow = s0 + (cv ? c / a.G : 0);
+    const int head = h * a.G + (cv ? c % a.G : 0);
+    if (a.splits > 1) {
+        if (!cv) return;
+        const int64_t rows = (int64_t)a.total * a.hq, at = split * rows + qrow * a.hq + head;
+        if (hh == 0) {
+            a.ws_ml[2 * at] = mrun;
+            a.ws_ml[2 * at + 1] = lrun;
         }
-        wave_lds_sync();
+        if (mrun == neg_inf()) return;
 #pragma unroll
-        for (int it = 0; it < kOutCols / RW; ++it) {
-            const int cc = it * RW + r, cr = c0 + half * 16 + cc;
-            const float *row = so + cc * (D + 4);
-            const float4 u = *reinterpret_cast<const float4 *>(row + 8 * j), v = *reinterpret_cast<const float4 *>(row + 8 * j + 4);
-            float o[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-            const float mx = row[D], l = row[D + 1];
-            const int64_t qrow = s0 + cr / a.G;
-            const int head = h * a.G + cr % a.G;
-            if (a.splits == 1) finish_row<D, ROT>(a, qrow, head, j, o, mx, l, cr < ncol);
-            else if (cr < ncol) {
-                const int64_t rows = (int64_t)a.total * a.hq, at = split * rows + qrow * a.hq + head;
-                if (j == 0) {
-                    a.ws_ml[2 * at] = mx;
-                    a.ws_ml[2 * at + 1] = l;
-                }
-                if (mx != neg_inf()) {
-                    float4 *p = reinterpret_cast<float4 *>(a.ws_part + at * D + 8 * j);
-                    p[0] = make_float4(o[0], o[1], o[2], o[3]);
-                    p[1] = make_float4(o[4], o[5], o[6], o[7]);
-                }
+        for (int i = 0; i < NF; ++i)
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+                *reinterpret_cast<float4 *>(a.ws_part + at * D + 32 * i + 8 * y + 4 * hh) =
+                    make_float4(acc[i][4 * y] * vunit, acc[i][4 * y + 1] * vunit, acc[i][4 * y + 2] * vunit, acc[i][4 * y + 3] * vunit);
+        return;
+    }
+    const float inv = lrun == 0.f ? 0.f : vunit / lrun;
+#pragma unroll
+    for (int i = 0; i < NF; ++i) acc[i] *= inv;
+    const RowEnd fin = cv ? row_end(a, qrow * a.hq + head, mrun, lrun) : RowEnd{0.f, 0.f, 0.f};
+    if (cv && a.lse && hh == 0) a.lse[qrow * a.hq + head] = fin.lse;
+    if constexpr (ROT) {
+        // back through H: the sums in two bf16 parts (2^-16 of the row's largest) times
+        // +-1; element e of step t is feature 16 t + 8 (e / 4) + 4 hh + e % 4
+        bf16x8 hi[NK], lo[NK];
+#pragma unroll
+        for (int t = 0; t < NK; ++t) {
+            uint32_t u[4], v[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float x0 = acc[t / 2][8 * (t & 1) + 2 * r], x1 = acc[t / 2][8 * (t & 1) + 2 * r + 1];
+                u[r] = bf16_pair(x0, x1);
+                v[r] = bf16_pair(x0 - __uint_as_float(u[r] << 16), x1 - __uint_as_float(u[r] & 0xFFFF0000u));
             }
+            hi[t] = __builtin_bit_cast(bf16x8, make_uint4(u[0], u[1], u[2], u[3]));
+            lo[t] = __builtin_bit_cast(bf16x8, make_uint4(v[0], v[1], v[2], v[3]));
         }
-        wave_lds_sync();
+        const float isd = D == 128 ? 0.08838834764831845f : 0.125f;
+#pragma unroll
+        for (int i = 0; i < NF; ++i) {
+            const uint32_t f = 32 * i + mtok;
+            const uint32_t b[4] = {sign_ones(f, 0), sign_ones(f, 2), sign_ones(f, 8), sign_ones(f, 10)};
+            f32x16 y{};
+#pragma unroll
+            for (int t = 0; t < NK; ++t) {
+                const bf16x8 hf = sign_frag(b, f, 16 * t + 4 * hh);
+                y = __builtin_amdgcn_mfma_f32_32x32x16_bf16(hf, hi[t], y, 0, 0, 0);
+                y = __builtin_amdgcn_mfma_f32_32x32x16_bf16(hf, lo[t], y, 0, 0, 0);
+            }
+            if (cv)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const uint32_t sb = sign_byte(a.c.sv, 4 * i + 2 * t + hh);
+                    float o[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[e] = flip(y[8 * t + e] * isd, (sb >> e) & 1);
+                    store_out8<D>(a, qrow, head, 32 * i + 16 * t + 8 * hh, o, fin);
+                }
+        }
+    } else {
+        // pieces of 4 features: this lane's and those of its neighbour half make pieces of 8
+#pragma unroll
+        for (int i = 0; i < NF; ++i)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                // registers 8 t + 0..3: features 16 t + 4 hh ..; 8 t + 4..7: 16 t + 8 + 4 hh ..
+                float o[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float a0 = acc[i][8 * t + e], a1 = acc[i][8 * t + 4 + e];
+                    const float other = __shfl_xor(hh ? a0 : a1, 32);
+                    o[e] = hh ? other : a0;
+                    o[4 + e] = hh ? a1 : other;
+                }
+                if (cv) store_out8<D>(a, qrow, head, 32 * i + 16 * t + 8 * hh, o, fin);
+            }
     }
 }
 
