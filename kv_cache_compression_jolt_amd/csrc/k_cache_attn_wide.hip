@@ -119,7 +119,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
     constexpr int kKStride = kTile * 16 + 32;          // bytes of a K chunk (8 features of 64 tokens), padded
     constexpr int kKBytes = D / 8 * kKStride, kVBytes = kTile / 8 * D * 16;
     constexpr int kSBytes = kPost ? NG * kTile * 4 : 0;
-    constexpr int kVBuf = kVBytes + kSBytes;           // the K scales of 8-bit codes lie behind V
+    constexpr int kVBuf = kVBytes + kSBytes + 2 * kTile * 4;      // behind V: K scales of 8-bit codes, a wild tile's units
     constexpr int kMain = 2 * kKBytes + 3 * kVBuf;
     constexpr bool kLo = ROT;                          // the queries' second parts stay in LDS: a lane's own fragments
     __shared__ __align__(16) uint8_t lds[kMain + (kLo ? NW * NK * 1024 : 0)];
@@ -253,7 +253,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
 #pragma unroll
     for (int i = 0; i < NF; ++i) acc[i] = f32x16{};
     float mrun = neg_inf(), lrun = 0.f;
-    int erun = kTop;                                   // exponent field of acc's unit: the largest V scale so far
+    int erun = kTop;                                   // exponent field of acc's unit, by column
     const float mul = a.scale * kLog2e * qmul;
     const bool capped = a.cap > 0.f, sloped = a.slopes != nullptr, tree = a.tree != nullptr;
 
@@ -322,13 +322,29 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
         rg.all[0] = __builtin_amdgcn_raw_buffer_load_b32(block(p0), all_off, i0 * 2, 0);
         rg.all[1] = __builtin_amdgcn_raw_buffer_load_b32(block(p1), all_off, i1 * 2, 0);
     };
-    // registers -> LDS; returns the exponent field of the tile's K unit, and raises enext
-    int enext = kTop;                                  // (the floor keeps a zero scale zero)
+    // Of the scales of K (lane 31) and of V (lane 63): the largest in the lower half,
+    // the smallest that is not 0 in the upper one, negated, so that one maximum over
+    // rows of 16 and then the second row of each half finds both.
+    auto extremes = [&](uint32_t a0, uint32_t a1) {
+        const u16x2 z{0, 0}, b0 = __builtin_bit_cast(u16x2, a0), b1 = __builtin_bit_cast(u16x2, a1);
+        const uint32_t x = pk_umax(a0, a1), y = pk_umax(__builtin_bit_cast(uint32_t, (u16x2)(z - b0)), __builtin_bit_cast(uint32_t, (u16x2)(z - b1)));
+        uint32_t v = pk_umax(__builtin_amdgcn_perm(y, x, 0x05040100u), __builtin_amdgcn_perm(y, x, 0x07060302u));
+        v = pk_umax(v, dpp_u<kDppXor1>(v));
+        v = pk_umax(v, dpp_u<kDppXor2>(v));
+        v = pk_umax(v, dpp_u<kDppHalfMirror>(v));
+        v = pk_umax(v, dpp_u<kDppMirror>(v));
+        return pk_umax(v, dpp_u<kDppRowBcast15>(v));
+    };
+    auto lane_of = [](uint32_t v, int l) { return (uint32_t)__builtin_amdgcn_readlane((int)v, l); };
+    // registers -> LDS.  Sets the tile's K and V units (exponent fields) and whether
+    // its scales spread too far for one unit (wild: every token then has its own).
+    int vunit_now = 0;                                 // V unit of the last tile, 0: none yet
     uint32_t magic = 0x64006400u;
     asm("" : "+v"(magic));
-    auto stage = [&](int t, int p0, int p1, uint8_t *kbuf, uint8_t *vbuf) -> int {
-        const int t0 = t * kTile;
-        const int lim0 = p0 >= 0 ? len : 0, lim1 = p1 >= 0 ? len : 0;      // tokens below these count, by half
+    struct Tile { int t, p0, p1, ek, ev, wild; };
+    auto stage = [&](Tile &tile, uint8_t *kbuf, uint8_t *vbuf) {
+        const int t0 = tile.t * kTile;
+        const int lim0 = tile.p0 >= 0 ? len : 0, lim1 = tile.p1 >= 0 ? len : 0;      // tokens below these count, by half
         const bool whole = t0 + kTile <= min(lim0, lim1);
         uint32_t all0 = rg.all[0], all1 = rg.all[1];
         if (!whole) {
@@ -336,17 +352,11 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
             all0 &= (ta < lim0 ? 0xFFFFu : 0u) | (ta + 1 < lim0 ? 0xFFFF0000u : 0u);
             all1 &= (tb < lim1 ? 0xFFFFu : 0u) | (tb + 1 < lim1 ? 0xFFFF0000u : 0u);
         }
-        // largest scale of K (lanes 0..31) and V (32..63): rows of 16, then the second row of each half
-        uint32_t x = pk_umax(all0, all1);
-        x = pk_umax(x, dpp_u<kDppXor1>(x));
-        x = pk_umax(x, dpp_u<kDppXor2>(x));
-        x = pk_umax(x, dpp_u<kDppHalfMirror>(x));
-        x = pk_umax(x, dpp_u<kDppMirror>(x));
-        x = pk_umax(x, dpp_u<kDppRowBcast15>(x));
-        const uint32_t xk = (uint32_t)__builtin_amdgcn_readlane((int)x, 31), xv = (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
-        int ek = (int)(max(xk & 0xFFFFu, xk >> 16) >> 7), ev = (int)(max(xv & 0xFFFFu, xv >> 16) >> 7);
-        const bool clean = whole && ek < 255 && ev < 255;
+        uint32_t x = extremes(all0, all1);
+        uint32_t xk = lane_of(x, 31), xv = lane_of(x, 63);
+        const bool clean = whole && max(xk & 0xFFFFu, xv & 0xFFFFu) < 0x7F80u;
         uint32_t kbad = 0;
+        const int limw = second ? lim1 : lim0, tk = t0 + ktok, tv = t0 + 8 * vblk;
         if (!clean) {
             // a tile with a last token, a missing half or a NaN scale inside: scales
             // that do not count become 0, and a NaN of K or V goes into the K row
@@ -355,17 +365,12 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
                 if (tt + 1 >= lim || (two & 0x7F800000u) == 0x7F800000u) two &= 0x0000FFFFu;
                 return two;
             };
-            x = pk_umax(finite(all0, 0, 2), finite(all1, 0, 2));
-            x = pk_umax(x, dpp_u<kDppXor1>(x));
-            x = pk_umax(x, dpp_u<kDppXor2>(x));
-            x = pk_umax(x, dpp_u<kDppHalfMirror>(x));
-            x = pk_umax(x, dpp_u<kDppMirror>(x));
-            x = pk_umax(x, dpp_u<kDppRowBcast15>(x));
-            const uint32_t yk = (uint32_t)__builtin_amdgcn_readlane((int)x, 31), yv = (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
-            ek = (int)(max(yk & 0xFFFFu, yk >> 16) >> 7);
-            ev = (int)(max(yv & 0xFFFFu, yv >> 16) >> 7);
-            const int limw = second ? lim1 : lim0, tk = t0 + ktok, tv = t0 + 8 * vblk;
-            const int pw = second ? p1 : p0;
+            all0 = finite(all0, 0, 2);
+            all1 = finite(all1, 0, 2);
+            x = extremes(all0, all1);
+            xk = lane_of(x, 31);
+            xv = lane_of(x, 63);
+            const int pw = second ? tile.p1 : tile.p0;
             if (tk < limw) {                           // limw > 0: the half has a page
                 const uint8_t *sv = a.c.pool + cache_block_offset(a.c, max(pw, 0), h) + pl.v_scales;
                 const uint32_t vs0 = reinterpret_cast<const uint16_t *>(sv)[tk & (P - 1)];
@@ -379,9 +384,41 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
 #pragma unroll
                 for (int i = 0; i < 4; ++i) rg.vs[q][i] = finite(rg.vs[q][i], tv + 2 * i, limw);
         }
-        ek = max(ek, kTop);
-        enext = max(enext, ev);
-        const uint32_t kdown = (uint32_t)(ek - kTop) * 0x00800080u, vdown = (uint32_t)(enext - kTop) * 0x00800080u;
+        // exponents of the largest scales and of the smallest (none: 512)
+        const uint32_t zv = xv & 0xFFFFu;
+        const int ek = max((int)((xk & 0xFFFFu) >> 7), kTop), ev = max((int)(zv >> 7), kTop);
+        const int lk = (int)((0x10000u - (xk >> 16)) >> 7), lv = (int)((0x10000u - (xv >> 16)) >> 7);
+        // V keeps its unit from tile to tile while the largest scale is at most 2^8
+        // below it, and raises it by up to 2^4; scales more than 2^18 below count fully
+        // only where every token has its own unit
+        const bool jump = vunit_now != 0 && (ev > vunit_now + 4 || ev < vunit_now - 8) && zv != 0;
+        if (zv != 0) vunit_now = jump || vunit_now == 0 ? ev : max(vunit_now, ev);
+        const int vu = max(vunit_now, kTop);
+        tile.wild = jump || (!kPost && lk < ek - 18) || lv < vu - 18;
+        tile.ek = ek;
+        tile.ev = tile.wild ? ev : vu;
+        uint32_t kdown = (uint32_t)(ek - kTop) * 0x00800080u;
+        uint32_t vdown[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) vdown[i] = (uint32_t)(vu - kTop) * 0x00800080u;
+        if (tile.wild) {
+            float *km = reinterpret_cast<float *>(vbuf + kVBytes + kSBytes);
+            int *ve = reinterpret_cast<int *>(km + kTile);
+            const int e = max((int)(max((uint32_t)rg.ks[0], (uint32_t)rg.ks[NG - 1]) >> 7), kTop);
+            const int ec = kbad ? kTop : e;            // (a NaN scale's exponent is no unit)
+            kdown = (uint32_t)(ec - kTop) * 0x00800080u;
+            if (ku0 == 0) km[ktok] = __builtin_ldexpf(1.f, ec - 127 - (kTop - 15));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t two = NG == 1 ? rg.vs[0][i] : pk_umax(rg.vs[0][i], rg.vs[NG - 1][i]);
+                const int e0 = max((int)((two >> 7) & 255u), kTop), e1 = max((int)(two >> 23), kTop);
+                vdown[i] = (uint32_t)(e0 - kTop) * 0x80u + (uint32_t)(e1 - kTop) * 0x00800000u;
+                if (vf == 0) {
+                    ve[8 * vblk + 2 * i] = e0;
+                    ve[8 * vblk + 2 * i + 1] = e1;
+                }
+            }
+        }
 #pragma unroll
         for (int x = 0; x < UPT; ++x) {
             const int u = ku0 + x, g = u / (D / 32), kk = u % (D / 32);
@@ -408,7 +445,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
 #pragma unroll
         for (int q = 0; q < NG; ++q)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sc[q][i] = scale_f16(rg.vs[q][i], vdown);
+            for (int i = 0; i < 4; ++i) sc[q][i] = scale_f16(rg.vs[q][i], vdown[i]);
 #pragma unroll
         for (int x = 0; x < UPT; ++x) {
             f16x2 y[4];
@@ -419,7 +456,6 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
             *reinterpret_cast<uint4 *>(vbuf + (vblk * D + vf + FS * x) * 16) =
                 make_uint4(u32(y[0]), u32(y[1]), u32(y[2]), u32(y[3]));
         }
-        return ek;
     };
 
     uint8_t *const vlds = lds + 2 * kKBytes;
@@ -434,23 +470,20 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
     // Both halves of tile i are staged before turn 2 i.  A turn that stages tile
     // i overlaps products on K(i-1) and V(i-2): two K buffers, three V buffers.
     const bool late = second;
-    struct Tile { int t, p0, p1, ek, ev; };
     auto look = [&](int t) {
-        if (t >= te) return Tile{t, -1, -1, kTop, kTop};
+        if (t >= te) return Tile{t, -1, -1, kTop, kTop, 0};
         if (t >= seen + 32) {
             seen = t;
             load_pages();
         }
-        return Tile{t, page_of(t, 0), page_of(t, 1), kTop, kTop};
+        return Tile{t, page_of(t, 0), page_of(t, 1), kTop, kTop, 0};
     };
     // field by field: a choice between the structs themselves would put them in memory
     auto of_group = [&](Tile e, Tile l) {
-        return Tile{late ? l.t : e.t, late ? l.p0 : e.p0, late ? l.p1 : e.p1, late ? l.ek : e.ek, late ? l.ev : e.ev};
+        return Tile{late ? l.t : e.t, late ? l.p0 : e.p0, late ? l.p1 : e.p1, late ? l.ek : e.ek, late ? l.ev : e.ev,
+                    late ? l.wild : e.wild};
     };
-    auto stage_tile = [&](Tile &x, int nth) {
-        x.ek = stage(x.t, x.p0, x.p1, lds + (nth & 1) * kKBytes, vlds + (nth % 3) * kVBuf);
-        x.ev = enext;
-    };
+    auto stage_tile = [&](Tile &x, int nth) { stage(x, lds + (nth & 1) * kKBytes, vlds + (nth % 3) * kVBuf); };
     f32x16 s[2];
     f16x8 pf[4];
     // In both products the next step's fragments are read from LDS before the
@@ -548,23 +581,27 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
             fetch(f.t, f.p0, f.p1);
         }
         times_k(0);
+        erun = cur.ev;
         __syncthreads();
         for (int i = 0;; ++i) {
             const int t0 = cur.t * kTile;
             const Tile nx3 = look(next_tile(nx2.t + 1));
             // ---- V: softmax of this tile, staging of a later one
-            if (cur.ev > erun) {                   // the V unit grew
-                const float f = __builtin_ldexpf(1.f, erun - cur.ev);
+            const float *km = reinterpret_cast<const float *>(vlds + (i % 3) * kVBuf + kVBytes + kSBytes) + 8 * hh;
+            float kunit = kPost ? 1.f : __builtin_ldexpf(1.f, cur.ek - 127 - (kTop - 15));   // 2^E
+            if (!kPost && cur.wild) {                  // a unit for every token
+                kunit = 1.f;
 #pragma unroll
-                for (int x = 0; x < NF; ++x) acc[x] *= f;
-                erun = cur.ev;
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) s[u][e] *= km[32 * u + (e >> 3) * 16 + (e & 7)];
             }
-            const float kunit = kPost ? 1.f : __builtin_ldexpf(1.f, cur.ek - 127 - (kTop - 15));   // 2^E
-            // scores in units of smul (log2 e times the scale's factors), or, where
-            // the terms are not linear, in log2 units already
-            float unit = mul * kunit;
+            // scores in units of `unit` (log2 e times the scale's factors; not so small that
+            // a masked score's -inf would meet a 0), or, where the terms are not linear, in
+            // log2 units already
+            float unit = fmaxf(mul * kunit, 1e-30f);
             if (capped) {
-                const float scap = unit * (2.f / a.cap);
+                const float scap = mul * kunit * (2.f / a.cap);
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -619,25 +656,83 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
 #pragma unroll
                 for (int x = 0; x < NF; ++x) acc[x] *= alpha;
             }
-            const float mu = mrun == neg_inf() ? 0.f : -mrun;
+            float mu = mrun == neg_inf() ? 0.f : -mrun, lsum = 0.f;
+            const bool shift = cur.wild || __any(erun != cur.ev);
+            if (shift || __any(fabsf(mu) > 1e6f)) {
+                // scores so large that their own rounding counts, and weights in another
+                // unit, take the difference to the maximum here
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) s[u][e] = s[u][e] * unit + mu;
+                unit = 1.f;
+                mu = 0.f;
+                if (shift) {
+                    // Another unit of V.  A column takes the tile's, unless its sum would leave
+                    // 2^-40 .. 2^100 there or every token has its own: then the one in which its
+                    // largest weight is 1 to 2, or its sum at 2^100 if that is larger (what the
+                    // other side then loses is below 2^-60 of the whole).
+                    float top = neg_inf(), atop = 0.f;
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) lsum += __builtin_amdgcn_exp2f(s[u][e]);
+                    if (cur.wild) {
+                        const int *ve = reinterpret_cast<const int *>(km + kTile);
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) s[u][e] += (float)(ve[32 * u + (e >> 3) * 16 + (e & 7)] - cur.ev);
+                    }
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) top = fmaxf(top, s[u][e]);
+#pragma unroll
+                    for (int x = 0; x < NF; ++x)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) atop = fmaxf(atop, fabsf(acc[x][e]));
+                    top = fmaxf(top, __shfl_xor(top, 32));
+                    atop = fmaxf(atop, __shfl_xor(atop, 32));
+                    constexpr int kNone = -4096;
+                    const int we = top > -1000.f ? cur.ev + (int)floorf(top) : kNone;
+                    const int ae = atop > 0.f ? erun + (int)(__float_as_uint(atop) >> 23) - 127 : kNone;
+                    int en = max(we, ae - 100);
+                    if (en <= kNone || (!cur.wild && (ae == kNone || (ae >= cur.ev - 40 && ae <= cur.ev + 100)))) en = cur.ev;
+#pragma unroll
+                    for (int x = 0; x < NF; ++x)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) acc[x][e] = __builtin_ldexpf(acc[x][e], erun - en);
+                    mu = (float)(cur.ev - en);
+                    erun = en;
+                    lsum += lrun;
+                }
+                asm("" : "+v"(s[0]), "+v"(s[1]));      // in place: no copies on the way past
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    s[u][e] = __builtin_amdgcn_exp2f(fmaf(s[u][e], unit, mu));
+                    lrun += s[u][e];
+                }
+            if (shift) lrun = lsum;
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                float p[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    p[e] = __builtin_amdgcn_exp2f(fmaf(s[x >> 1][8 * (x & 1) + e], unit, mu));
-                    lrun += p[e];
-                }
-                pf[x] = __builtin_bit_cast(f16x8, make_uint4(f16_pair(p[0], p[1]), f16_pair(p[2], p[3]),
-                                                             f16_pair(p[4], p[5]), f16_pair(p[6], p[7])));
+                const f32x16 &p = s[x >> 1];
+                const int o = 8 * (x & 1);
+                pf[x] = __builtin_bit_cast(f16x8, make_uint4(f16_pair(p[o], p[o + 1]), f16_pair(p[o + 2], p[o + 3]),
+                                                             f16_pair(p[o + 4], p[o + 5]), f16_pair(p[o + 6], p[o + 7])));
                 asm volatile("" : "+v"(pf[x]), "+v"(lrun));   // computed in this turn, not sunk into the next
             }
             Tile st = of_group(nxt, nx2);
             stage_tile(st, late ? i + 2 : i + 1);
             nxt.ek = late ? nxt.ek : st.ek;
             nxt.ev = late ? nxt.ev : st.ev;
+            nxt.wild = late ? nxt.wild : st.wild;
             nx2.ek = late ? st.ek : nx2.ek;
             nx2.ev = late ? st.ev : nx2.ev;
+            nx2.wild = late ? st.wild : nx2.wild;
             __syncthreads();
             // ---- M: products
             const bool last = nxt.t >= te;
@@ -660,7 +755,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
     // ---- rows out: lane (column m, half hh) has features 32 i + 8 (j / 4) + 4 hh + j % 4
     if (!active) return;
     lrun += __shfl_xor(lrun, 32);
-    const float vunit = __builtin_ldexpf(1.f, erun - 127 - (kTop - 15));
+    const int vexp = erun - 127 - (kTop - 15);
     const int64_t qrow = s0 + (cv ? c / a.G : 0);
     const int head = h * a.G + (cv ? c % a.G : 0);
     if (a.splits > 1) {
@@ -676,12 +771,15 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
 #pragma unroll
             for (int y = 0; y < 4; ++y)
                 *reinterpret_cast<float4 *>(a.ws_part + at * D + 32 * i + 8 * y + 4 * hh) =
-                    make_float4(acc[i][4 * y] * vunit, acc[i][4 * y + 1] * vunit, acc[i][4 * y + 2] * vunit, acc[i][4 * y + 3] * vunit);
+                    make_float4(__builtin_ldexpf(acc[i][4 * y], vexp), __builtin_ldexpf(acc[i][4 * y + 1], vexp),
+                                __builtin_ldexpf(acc[i][4 * y + 2], vexp), __builtin_ldexpf(acc[i][4 * y + 3], vexp));
         return;
     }
-    const float inv = lrun == 0.f ? 0.f : vunit / lrun;
+    const float inv = lrun == 0.f ? 0.f : 1.f / lrun;
 #pragma unroll
-    for (int i = 0; i < NF; ++i) acc[i] *= inv;
+    for (int i = 0; i < NF; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][e] = __builtin_ldexpf(acc[i][e] * inv, vexp);
     const RowEnd fin = cv ? row_end(a, qrow * a.hq + head, mrun, lrun) : RowEnd{0.f, 0.f, 0.f};
     if (cv && a.lse && hh == 0) a.lse[qrow * a.hq + head] = fin.lse;
     if constexpr (ROT) {

@@ -365,6 +365,15 @@ def test_rows_that_see_nothing(shape):
 
 
 @pytest.mark.parametrize("shape", SHAPES, ids=IDS)
+def test_split_rows_many(shape):
+    """The same for more query rows (the kernel of many columns), and few rows in many ranges."""
+    c = filled(shape, [1700, 20, 1100])
+    attend_and_check(c, [40, 20, 3], 2)
+    attend_and_check(c, [33, 1, 2], 2, window=900, prefix=[3, 0, 70], merge=True, cap=10.0)
+    attend_and_check(c, [1, 1, 1], 1, max_len=10 ** 6)
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=IDS)
 def test_split_rows(shape):
     """Caches long enough to be cut into ranges, joined by the second launch."""
     c = filled(shape, [1500, 700, 20])
@@ -413,9 +422,57 @@ def test_garbage_in_masked_places():
     assert bool(c.torch.isnan(out).all())
 
 
+@pytest.mark.parametrize("shape", SHAPES, ids=IDS)
+@pytest.mark.parametrize("n", [3, 45])
+def test_scales_far_apart(shape, n):
+    """Huge and tiny rows: masked ones (another document, 1e20 times larger or smaller) change nothing
+    for the rows that do not see them, and visible values of any size are summed in full."""
+    s = oc.Shape(*shape, seed=3)
+    for far in (1e20, 1e-20):
+        c = Both(s, 1, (200 + s.P - 1) // s.P, 8, seed=1)
+        rng = np.random.default_rng(7)
+        k, v = (rng.standard_normal((200, s.H, s.d)) for _ in range(2))
+        k[:75] *= far
+        v[:75] *= far
+        c.set_lens([200])
+        c.append(bf16(k), bf16(v), [200])
+        attend_and_check(c, [n], 2, first=[75] * n)
+        attend_and_check(c, [n], 2, window=100)
+        v = v * 2.0 ** rng.integers(-30, 30, (200, 1, 1))
+        c.append(bf16(rng.standard_normal(k.shape)), bf16(v), [200])
+        attend_and_check(c, [n], 2)
+        attend_and_check(c, [n], 2, cap=4.0, slopes=True, first=[75] * n)
+
+
+@pytest.mark.parametrize("n", [3, 45])
+def test_zero_and_large_queries(n):
+    for shape in (SHAPES[0], SHAPES[3], SHAPES[5]):
+        c = filled(shape, [150, 80])
+        rng = np.random.default_rng(n)
+        q = bf16(rng.standard_normal((2 * n + 3, shape[0] * 2, shape[1])))
+        q[::3] = 0
+        attend_and_check(c, [n, n], 2, q=q)
+        q[1::3] = bf16(q[1::3] * 1e-30)
+        attend_and_check(c, [n, n], 2, q=q, cap=3.0, window=60)
+        attend_and_check(c, [n, n], 2, q=bf16(q * 1e15), scale=1e-16)
+
+
+def test_rows_and_keys_of_zeros():
+    s = oc.Shape(2, 128, 4, 64, True)
+    c = Both(s, 1, 4, 4)
+    rng = np.random.default_rng(0)
+    k, v = (bf16(rng.standard_normal((190, 2, 128))) for _ in range(2))
+    k[:64], v[64:128] = 0, 0
+    c.set_lens([190])
+    c.append(k, v, [190])
+    for n in (2, 40):
+        attend_and_check(c, [n], 2)
+
+
 def test_bad_pages_are_left_out():
     c = filled((2, 64, 8, 32, True), [120, 70], max_pages=4, bad=((0, 1, 1000), (0, 2, -1), (1, 0, -7)))
     attend_and_check(c, [3, 2], 2)
+    attend_and_check(c, [30, 40], 2)
     c.set_lens([500, 70])                                       # longer than the table row
     out = c.torch.empty(2, 2, 64, dtype=c.torch.bfloat16, device="cuda")
     c.gpu.attention(c.dev(np.ones((2, 2, 64)), "bf16"), c.i32([0, 1, 2]), 1, 500, out)
