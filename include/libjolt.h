@@ -358,9 +358,9 @@ jolt_status jolt_cache_keep(jolt_handle h, const jolt_cache *cache, int32_t batc
  *           over the payloads of the same sequence, joined into the result by
  *           the two log-sum-exps */
 typedef struct {
-    float scale;
-    float cap;
-    int32_t window;
+    float scale;             /* > 0                                             */
+    float cap;               /* 0: none; scale / cap within fp32                 */
+    int32_t window;          /* 0: none                                         */
     int32_t reserved;
     const float *slopes;
     const int32_t *prefix;
@@ -380,10 +380,11 @@ typedef struct {
  * products exactly; rotated queries are held in two parts (2^-16 or better);
  * weights, with their value scales, are rounded to bf16 (few query rows) or
  * fp16 (many); sums and softmax statistics are fp32.  A visible token stored as
- * NaN makes the row's output NaN (its lse may be, too).  The workspace (jolt_cache_attention_workspace_size() bytes for the
- * same sizes, 16-byte aligned) carries split rows from launch to launch: calls
- * that may overlap (other streams, or replays of captured graphs) need one
- * each. */
+ * NaN makes the row's output NaN (its lse may be, too), and so do a query with an
+ * infinity or a NaN, a score past 2^127, and sums of values past 2^110.  The
+ * workspace (jolt_cache_attention_workspace_size() bytes for the same sizes,
+ * 16-byte aligned) carries split rows from launch to launch: calls that may
+ * overlap (other streams, or replays of captured graphs) need one each. */
 jolt_status jolt_cache_attention_workspace_size(const jolt_cache *cache, int32_t batch, int32_t total, int32_t max_q,
                                                 int32_t max_len, int32_t q_heads, size_t *bytes);
 jolt_status jolt_cache_attention(jolt_handle h, const jolt_cache *cache, int32_t batch, const int32_t *starts,

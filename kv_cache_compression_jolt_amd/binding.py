@@ -487,12 +487,12 @@ class JoltCache:
 
     Holds a handle, the caller's pool (uint8), page table (int32 [batch,
     max_pages]) and lengths (int32 [batch]), and a workspace for split
-    attention rows for each stream that calls come on.  The tensors stay the
-    caller's: update `lens` (and `table`) in place between calls; rows of a
+    attention rows for each stream that calls come on (a captured call keeps one
+    of its own, so that graphs may be replayed side by side).  The tensors stay
+    the caller's: update `lens` (and `table`) in place between calls; rows of a
     call count as the last tokens of their sequence.  Calls go to the current
-    stream of the cache's device.  Captured graphs that may be replayed side by
-    side pass a `workspace` of their own each (uint8, at least
-    workspace_bytes(...) long).
+    stream of the cache's device.  A caller's own `workspace` is a uint8 tensor
+    of at least workspace_bytes(...) bytes.
     """
 
     def __init__(self, H, d, bits, pool, table, lens, page_tokens=64, rotate=True, seed=0, k_item_id=0, v_item_id=1):
@@ -500,6 +500,8 @@ class JoltCache:
         self.torch = torch
         self.h = None
         self.device = pool.device
+        if self.device.type != "cuda":
+            raise ValueError("pool must be a tensor on a GPU")
         for name, t, dt, dims in (("pool", pool, torch.uint8, None), ("table", table, torch.int32, 2),
                                   ("lens", lens, torch.int32, 1)):
             self._tensor(name, t, dt, dims)
@@ -513,6 +515,7 @@ class JoltCache:
         self.c, self.pool, self.table, self.lens = c, pool, table, lens
         self.batch, self.H, self.d = int(lens.shape[0]), H, d
         self.workspaces = {}          # stream -> every workspace it has used, the last one the largest
+        self.captured = []            # workspaces of captured calls
         with torch.cuda.device(self.device):
             self.h = jolt_create(self.device.index)
 
@@ -591,10 +594,13 @@ class JoltCache:
         sp = self._tensor("starts", starts, i32, 1, self.batch + 1)
         stream = self._stream()
         own = workspace is None
-        if own:
+        with torch.cuda.device(self.device):
+            capturing = own and torch.cuda.is_current_stream_capturing()
+        if own and not capturing:
             have = self.workspaces.get(stream)
             workspace = have[-1] if have else None
-        elif workspace.device != self.device or workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
+        elif not own and (workspace.device != self.device or workspace.dtype is not torch.uint8 or
+                          not workspace.is_contiguous()):
             raise ValueError("workspace must be a contiguous uint8 tensor on %s" % (self.device,))
         if tree is not None:
             tp = self._tensor("tree", tree, torch.int64, None, total)
@@ -609,10 +615,10 @@ class JoltCache:
             if st != JOLT_E_WORKSPACE or not own or again:
                 break
             # refused before any launch: a larger workspace, and again.  None is
-            # dropped: a captured graph goes on using the one it was captured with
+            # dropped: launches may still be under way on it, or graphs replayed
             workspace = torch.empty(self.workspace_bytes(total, max_q, max_len, hq), dtype=torch.uint8,
                                     device=self.device)
-            self.workspaces.setdefault(stream, []).append(workspace)
+            (self.captured if capturing else self.workspaces.setdefault(stream, [])).append(workspace)
         _check(st, self.h)
 
     def attention(self, q, starts, max_q, max_len, out, lse=None, scale=None, cap=0.0, slopes=None, window=0,

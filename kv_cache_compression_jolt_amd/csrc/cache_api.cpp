@@ -104,6 +104,11 @@ static jolt_status attn_call(jolt_handle h, const jolt_cache *cache, int32_t bat
     if (!(terms->scale > 0.f) || !std::isfinite(terms->scale))
         return fail(h, JOLT_E_INVALID, "attention: scale must be > 0");
     if (!(terms->cap >= 0.f) || !std::isfinite(terms->cap)) return fail(h, JOLT_E_INVALID, "attention: cap must be >= 0");
+    // what the kernels multiply scores with, in log2 units and in the cap's
+    constexpr float kTwoLog2e = 2.8853901f;
+    if (!std::isfinite(terms->scale * kTwoLog2e) ||
+        (terms->cap > 0.f && (!std::isfinite(terms->scale / terms->cap * kTwoLog2e) || !std::isfinite(terms->cap * kTwoLog2e))))
+        return fail(h, JOLT_E_INVALID, "attention: scale, cap or scale / cap is beyond fp32");
     if (terms->window < 0) return fail(h, JOLT_E_INVALID, "attention: window must be >= 0");
     if (!terms->merge_out != !terms->merge_lse)
         return fail(h, JOLT_E_INVALID, "attention: merge_out and merge_lse go together");

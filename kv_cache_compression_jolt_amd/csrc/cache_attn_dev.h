@@ -9,6 +9,11 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 
+// The maximum of a part whose sum of weights is l: a part that met a NaN counts
+// above every other, so that no join leaves it out as a part that saw nothing (its
+// maximum may still be -infinity) or as one whose weights have vanished.
+__device__ __forceinline__ float nan_outweighs(float m, float l) { return l != l ? 3e38f : m; }
+
 // Which (sequence, KV head, columns, token range) a workgroup has.  Workgroups
 // go to the 8 XCDs in turn; all of one (sequence, head) stay on one XCD, whose L2
 // then serves its rows of the cache, and the units are dealt out one by one, so

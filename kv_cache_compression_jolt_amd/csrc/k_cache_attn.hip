@@ -319,6 +319,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_cache_attn(CacheAttnArgs a, 
     // ---- join the waves
     lrun += __shfl_xor(lrun, 16);
     lrun += __shfl_xor(lrun, 32);
+    mrun = nan_outweighs(mrun, lrun);
     if (g == 0) {
         sml[0][wave][m] = mrun;
         sml[1][wave][m] = lrun;

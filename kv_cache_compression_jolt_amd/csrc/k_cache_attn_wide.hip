@@ -254,7 +254,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
     for (int i = 0; i < NF; ++i) acc[i] = f32x16{};
     float mrun = neg_inf(), lrun = 0.f;
     int erun = kTop;                                   // exponent field of acc's unit, by column
-    const float mul = a.scale * kLog2e * qmul;
+    const float mul = fminf(a.scale * kLog2e * qmul, 3e38f);     // (finite: a score of 0 stays 0)
     const bool capped = a.cap > 0.f, sloped = a.slopes != nullptr, tree = a.tree != nullptr;
 
     // tiles between a prefix and the window are skipped by the whole workgroup
@@ -601,7 +601,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
             // log2 units already
             float unit = fmaxf(mul * kunit, 1e-30f);
             if (capped) {
-                const float scap = mul * kunit * (2.f / a.cap);
+                const float scap = fminf(a.scale / a.cap * (2.f * kLog2e) * qmul * kunit, 3e38f);
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -755,6 +755,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
     // ---- rows out: lane (column m, half hh) has features 32 i + 8 (j / 4) + 4 hh + j % 4
     if (!active) return;
     lrun += __shfl_xor(lrun, 32);
+    mrun = nan_outweighs(mrun, lrun);
     const int vexp = erun - 127 - (kTop - 15);
     const int64_t qrow = s0 + (cv ? c / a.G : 0);
     const int head = h * a.G + (cv ? c % a.G : 0);

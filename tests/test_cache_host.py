@@ -60,3 +60,11 @@ def test_attention_workspace_size():
     with pytest.raises(jb.JoltError) as e:
         jb.jolt_cache_attention_workspace_size(c, 1, 1, 1, 100, 12)
     assert e.value.status == jb.JOLT_E_INVALID
+
+
+def test_a_cache_lies_on_a_gpu():
+    import torch
+    i32 = torch.int32
+    with pytest.raises(ValueError):
+        jb.JoltCache(1, 64, 4, torch.zeros(4096, dtype=torch.uint8), torch.zeros(1, 1, dtype=i32),
+                     torch.zeros(1, dtype=i32))

@@ -703,6 +703,174 @@ def test_streams_side_by_side():
         assert t.equal(o, outs[0])
 
 
+def test_captured_prompt_tree_keep_and_read():
+    """A chunk of many query rows, a tree, its accepted path and the read captured in one graph, without a
+    workspace of the caller's, and replayed with other contents and lengths between replays."""
+    c = filled((2, 128, 4, 64, True), [1300, 900], max_pages=24)
+    t, s = c.torch, c.s
+    rng = np.random.default_rng(2)
+    n, G = 40, 2
+    k, v = (t.zeros(2 * n, s.H, s.d, dtype=t.bfloat16, device="cuda") for _ in range(2))
+    q = t.zeros(2 * n, s.H * G, s.d, dtype=t.bfloat16, device="cuda")
+    out, out2 = t.zeros_like(q), t.zeros_like(q)
+    lse = t.zeros(2 * n, s.H * G, device="cuda")
+    masks = t.tensor([(2 << i) - 1 for i in range(n)] * 2, dtype=t.int64, device="cuda")
+    st, base, first = c.i32([0, n, 2 * n]), c.i32([0, 0]), c.i32([0, 0])
+    kst, path = c.i32([0, 3, 5]), c.i32([0, 2, 3, 1, 30])
+    rst = c.i32([0, 70, 100])
+    rk, rv = (t.zeros(100, s.H, s.d, dtype=t.bfloat16, device="cuda") for _ in range(2))
+
+    def step(o, l, o2, a, b):
+        c.gpu.append(k, v, st, n)
+        c.gpu.attention(q, st, n, 1400, o, l, window=700)
+        c.gpu.tree_attention(q, st, n, 1400, masks, o2)
+        c.gpu.keep(base, kst, path)
+        c.gpu.read(first, rst, 70, a, b)
+    side = t.cuda.Stream()
+    side.wait_stream(t.cuda.current_stream())
+    with t.cuda.stream(side):
+        step(out, lse, out2, rk, rv)
+    t.cuda.synchronize()
+    graph = t.cuda.CUDAGraph()
+    with t.cuda.graph(graph):
+        step(out, lse, out2, rk, rv)
+    assert len(c.gpu.captured) > 0
+    for i in range(4):
+        lens = [1300 + 11 * i, 900 + 64 * i]
+        c.lens.copy_(c.i32(lens))
+        base.copy_(c.i32([x - n for x in lens]))
+        first.copy_(c.i32([x - n - 20 for x in lens]))
+        for x in (k, v, q):
+            x.copy_(c.dev(rng.standard_normal(tuple(x.shape)), "bf16"))
+        saved = c.pool.clone()
+        t.cuda.synchronize()
+        graph.replay()
+        t.cuda.synchronize()
+        after = c.pool.clone()
+        c.pool.copy_(saved)
+        eager = [t.zeros_like(x) for x in (out, lse, out2, rk, rv)]
+        step(*eager)
+        t.cuda.synchronize()
+        assert t.equal(after, c.pool)
+        for x, y in zip(eager, (out, lse, out2, rk, rv)):      # bits: tokens never written may be NaN
+            assert t.equal(x.view(t.int8), y.view(t.int8))
+
+
+def test_two_graphs_replayed_side_by_side():
+    c = filled((2, 128, 4, 64, True), [3000])
+    t = c.torch
+    st, q, outs, graphs = c.i32([0, 1]), [], [], []
+    for i in range(2):
+        q.append(c.dev(np.random.default_rng(i).standard_normal((1, 8, 128)), "bf16"))
+        outs.append(t.zeros_like(q[i]))
+    want = [t.zeros_like(x) for x in outs]
+    for i in range(2):
+        c.gpu.attention(q[i], st, 1, 3000, want[i])
+    t.cuda.synchronize()
+    for i in range(2):
+        g = t.cuda.CUDAGraph()
+        with t.cuda.graph(g):
+            for _ in range(20):
+                c.gpu.attention(q[i], st, 1, 3000, outs[i])
+        graphs.append(g)
+    streams = [t.cuda.Stream(), t.cuda.Stream()]
+    for _ in range(5):
+        for i in range(2):
+            outs[i].zero_()
+        t.cuda.synchronize()
+        for i in range(2):
+            with t.cuda.stream(streams[i]):
+                graphs[i].replay()
+        t.cuda.synchronize()
+        assert t.equal(outs[0], want[0]) and t.equal(outs[1], want[1])
+
+
+@pytest.mark.parametrize("n", [1, 45])
+def test_queries_that_are_not_numbers(n):
+    """A row with an infinity or a NaN is NaN; the others do not change."""
+    for shape in (SHAPES[0], SHAPES[5]):
+        c = filled(shape, [150, 80])
+        t, hq = c.torch, shape[0] * 2
+        st, q = c.i32([0, n, 2 * n]), c.dev(np.random.default_rng(n).standard_normal((2 * n, hq, shape[1])), "bf16")
+        clean, out = t.zeros_like(q), t.zeros_like(q)
+        c.gpu.attention(q, st, n, 150, clean)
+        q[0, 1, 5] = float("nan")
+        q[n, 0, 60] = float("inf")
+        c.gpu.attention(q, st, n, 150, out)
+        assert bool(out[0, 1].isnan().all()) and bool(out[n, 0].isnan().all())
+        same = t.ones(2 * n, hq, dtype=t.bool, device="cuda")
+        same[0, 1] = same[n, 0] = False
+        # (a neighbour may raise its running maximum at another block: one rounding of weights and output)
+        assert float((out - clean)[same].float().norm(dim=-1).max()) <= 2.0 ** -6 * float(clean.float().norm(dim=-1).max())
+
+
+@pytest.mark.parametrize("G", [1, 40])
+def test_nan_rows_that_stand_alone(G):
+    """A visible NaN row is not lost where it is all that a row, a wave or a token range sees, nor where every
+    other score is far above its part's."""
+    for shape in (SHAPES[0], SHAPES[5]):
+        s = oc.Shape(*shape, seed=3)
+        for T, at in ((1, 0), (40, 39), (9000, 4500), (9000, 8999)):
+            c = Both(s, 1, (T + s.P - 1) // s.P, (T + s.P - 1) // s.P)
+            k, v = (bf16(np.random.default_rng(x).standard_normal((T, s.H, s.d))) for x in (1, 2))
+            v[at, 0, 3] = np.nan
+            q = bf16(np.random.default_rng(3).standard_normal((1, s.H * G, s.d)))
+            k[at + 1:] += 100 * q[0, 0]
+            c.set_lens([T])
+            c.append(bf16(k), v, [T])
+            t = c.torch
+            out = t.zeros(1, s.H * G, s.d, dtype=t.bfloat16, device="cuda")
+            c.gpu.attention(c.dev(q, "bf16"), c.i32([0, 1]), 1, T, out)
+            nan = out.isnan()
+            assert bool(nan[:, :G].all()) and not bool(nan[:, G:].any())
+
+
+@pytest.mark.parametrize("shape", [SHAPES[0], SHAPES[7]], ids=[IDS[0], IDS[7]])
+def test_pages_past_4_gib(shape):
+    """The same tokens in pages at the two ends of a pool of more than 2^32 bytes."""
+    s = oc.Shape(*shape, seed=3)
+    jb, t = jolt_binding(), torch_cuda()
+    page = s.H * s.head_bytes
+    pages = (1 << 32) // page + 40
+    pool = t.zeros(pages * page, dtype=t.uint8, device="cuda")
+    n, T, lens = 40, 500, None
+    mp = (T + s.P - 1) // s.P
+    rng = np.random.default_rng(1)
+    k, v, q = (t.from_numpy(rng.standard_normal((x, h, s.d)).astype(np.float32)).cuda().bfloat16()
+               for x, h in ((T, s.H), (T, s.H), (n, 2 * s.H)))
+    starts, rows = (t.tensor([0, x], dtype=t.int32, device="cuda") for x in (T, n))
+    lens = t.tensor([T], dtype=t.int32, device="cuda")
+    got = []
+    for low in (0, pages - mp):
+        table = t.arange(low, low + mp, dtype=t.int32, device="cuda").view(1, mp)
+        g = jb.JoltCache(s.H, s.d, s.bits, pool, table, lens, page_tokens=s.P, rotate=s.rotate, seed=3)
+        g.append(k, v, starts, T)
+        g.keep(t.tensor([T - 20], dtype=t.int32, device="cuda"), t.tensor([0, 2], dtype=t.int32, device="cuda"),
+               t.tensor([4, 3], dtype=t.int32, device="cuda"))
+        outs = [t.zeros_like(q), t.zeros_like(q[:1]), t.zeros_like(k), t.zeros_like(v)]
+        g.attention(q, rows, n, T, outs[0])
+        g.attention(q[:1], t.tensor([0, 1], dtype=t.int32, device="cuda"), 1, T, outs[1])
+        g.read(None, starts, T, outs[2], outs[3])
+        t.cuda.synchronize()
+        got.append(outs)
+    assert bool(got[0][2].any()) and t.equal(pool[:mp * page], pool[(pages - mp) * page:])
+    for x, y in zip(*got):
+        assert t.equal(x, y)
+
+
+def test_more_refusals():
+    c = filled((2, 128, 4, 64, True), [20])
+    t, jb = c.torch, c.jb
+    st, q = c.i32([0, 1]), t.zeros(1, 4, 128, dtype=t.bfloat16, device="cuda")
+    # 2 log2 e = 2.885 times scale, scale / cap and cap has to stay below 3.403e38
+    for kw in (dict(scale=3e38), dict(scale=1.0, cap=8e-39), dict(scale=1.0, cap=3e38)):
+        with pytest.raises(jb.JoltError) as e:
+            c.gpu.attention(q, st, 1, 20, t.zeros_like(q), **kw)
+        assert e.value.status == jb.JOLT_E_INVALID
+    with pytest.raises(ValueError):
+        c.gpu.attention(q, st, 1, 20, t.zeros_like(q), workspace=t.zeros(64, device="cuda"))
+
+
 def test_empty_calls():
     s = oc.Shape(1, 64, 4, 32, True)
     c = Both(s, 1, 1, 1)
