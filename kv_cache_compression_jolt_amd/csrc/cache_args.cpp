@@ -73,13 +73,22 @@ jolt_status cache_attn_check(const jolt_cache *c, int32_t batch, int32_t total, 
     return JOLT_OK;
 }
 
-// Query columns of a KV head and sequence: up to 32 go to the narrow kernel
-// (tiles of 16), more to the wide one (tiles of 256).  Token ranges: enough
-// workgroups for the 256 CUs, none of fewer than 256 (512) tokens.
+// Narrow kernel (tiles of 16 query columns of a KV head and sequence, 4 waves) or
+// wide one (tiles of 256, one per CU).  The wide one computes a score for a third
+// less where it is busy, but its start and end cost 17 us against 8, and a tile
+// that is not full costs what a full one does.  8 heads, d = 128, 4 bits, narrow
+// against wide in us: 16 x 4096 tokens 116 : 127 at 128 columns, 145 : 129 at 160,
+// 221 : 138 at 256; 16 x 1024 tokens 56 : 56 at 192 columns; 16384 tokens 52 : 55
+// at 192 and 62 : 61 at 256; 4096 tokens 26 : 44 at 256.  So the wide one takes
+// more than 128 columns with more than 24 * 2^20 scores.
+// Token ranges: enough workgroups for the 256 CUs (two of the narrow kernel's share
+// one), none of fewer than 256 tokens (wide: 512).  A decode step in ranges of at
+// least 128, 256 and 512 tokens: 11.1, 11.4, 13.7 us at 1024 tokens, 14.4, 12.6
+// us at 4 x 2048 (128, 256); wide, 256 and 512 tokens: 60.9 and 59.9 us at 16384.
 AttnPlan cache_attn_plan(const jolt_cache &c, int batch, int64_t total, int max_q, int max_len, int q_heads) {
     AttnPlan p{};
     const int64_t cols = (int64_t)max_q * (q_heads / c.H);
-    p.wide = cols > 32;
+    p.wide = cols > 128 && (double)batch * c.H * cols * max_len > 24.0 * (1 << 20);
     const int64_t per = p.wide ? 256 : 16, want = p.wide ? 256 : 512, least = p.wide ? 512 : 256;
     const int64_t tiles = std::max<int64_t>(1, (int64_t)batch * c.H * ((cols + per - 1) / per));
     p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(max_len / least, want / tiles), 256));

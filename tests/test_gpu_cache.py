@@ -254,7 +254,8 @@ def reference(c, b, n, q, scale, cap=0.0, slopes=None, window=0, prefix=0, first
 
 
 def attend_and_check(c, n, G, scale=None, cap=0.0, slopes=False, window=0, prefix=None, first=None, tree=None,
-                     merge=False, q=None, max_len=None, spare=3, run=None, lse_wanted=True):
+                     merge=False, q=None, max_len=None, spare=3, run=None, lse_wanted=True, many=True):
+    """many: once more with a bound on the rows that picks the kernel of many query columns, where one does."""
     s, t = c.s, c.torch
     hq, st = s.H * G, c.starts(n)
     total = int(st[-1])
@@ -278,35 +279,48 @@ def attend_and_check(c, n, G, scale=None, cap=0.0, slopes=False, window=0, prefi
         ml = (rng.standard_normal((total + spare, hq)) + 4).astype(np.float32)
         ml[0, 0] = -np.inf
         kw["merge_out"], kw["merge_lse"] = t.from_numpy(mo).cuda(), t.from_numpy(ml).cuda()
-    args = [c.dev(q, "bf16"), c.i32(st), int(max(n)), max(c.ref.lens) if max_len is None else max_len]
-    if tree is not None:
-        m = np.array([x for row in tree for x in row] + [0] * spare, dtype=np.uint64).view(np.int64)
-        call = lambda: c.gpu.tree_attention(*args, t.from_numpy(m.copy()).cuda(), out, lse, **kw)  # noqa: E731
-    else:
-        call = lambda: c.gpu.attention(*args, out, lse, **kw)                                       # noqa: E731
-    (run or (lambda f: f()))(call)
-    t.cuda.synchronize()
-    go = out.float().cpu().numpy().astype(np.float64)
-    gl = lse.cpu().numpy().astype(np.float64) if lse_wanted else None
-    worst = 0.0
-    for b in range(c.batch):
-        r = slice(st[b], st[b + 1])
-        if n[b] == 0:
-            continue
-        o, l, eo, el = reference(c, b, n[b], q[r].astype(np.float64), scale, cap, sl, window,
-                                 0 if prefix is None else prefix[b], None if first is None else list(first)[r],
-                                 None if tree is None else tree[b],
-                                 (mo[r].astype(np.float64), ml[r].astype(np.float64)) if merge else None)
-        none, bad = np.isneginf(l), np.isnan(o).any(-1)              # bad: a NaN row is visible
-        assert np.all(go[r][none] == 0) and np.all(np.isnan(go[r][bad]))
-        err, eo = np.linalg.norm(np.where(bad[..., None], 0, go[r] - o), axis=-1), np.where(bad, 0, eo)
-        none |= bad
-        assert np.all(err <= eo + 1e-30), (b, np.max(err / (eo + 1e-30)))
-        worst = max(worst, float(np.max(err / (eo + 1e-30))))
+    max_len = max(c.ref.lens) if max_len is None else max_len
+    bounds = [int(max(n))]
+    big = 64 if tree is not None else (1 << 17) // G
+    if many and bounds[0] < big and big * G > 128:
+        bounds.append(big)
+    worst, refs = 0.0, {}
+    for max_q in bounds:
+        if max_q == big and tree is not None:
+            max_len = max(max_len, 1 << 20)              # few columns: more scores make it the kernel of many
+        args = [c.dev(q, "bf16"), c.i32(st), max_q, max_len]
+        out.fill_(7.0)
         if lse_wanted:
-            assert np.all(np.isneginf(gl[r][none & ~bad]))
-            assert np.all(np.abs(gl[r][~none] - l[~none]) <= el[~none])
-    assert np.all(go[total:] == 7.0) and (gl is None or np.all(gl[total:] == 7.0))
+            lse.fill_(7.0)
+        if tree is not None:
+            m = np.array([x for row in tree for x in row] + [0] * spare, dtype=np.uint64).view(np.int64)
+            call = lambda: c.gpu.tree_attention(*args, t.from_numpy(m.copy()).cuda(), out, lse, **kw)  # noqa: E731
+        else:
+            call = lambda: c.gpu.attention(*args, out, lse, **kw)                                       # noqa: E731
+        (run or (lambda f: f()))(call)
+        t.cuda.synchronize()
+        go = out.float().cpu().numpy().astype(np.float64)
+        gl = lse.cpu().numpy().astype(np.float64) if lse_wanted else None
+        for b in range(c.batch):
+            r = slice(st[b], st[b + 1])
+            if n[b] == 0:
+                continue
+            if b not in refs:
+                refs[b] = reference(c, b, n[b], q[r].astype(np.float64), scale, cap, sl, window,
+                                    0 if prefix is None else prefix[b], None if first is None else list(first)[r],
+                                    None if tree is None else tree[b],
+                                    (mo[r].astype(np.float64), ml[r].astype(np.float64)) if merge else None)
+            o, l, eo, el = refs[b]
+            none, bad = np.isneginf(l), np.isnan(o).any(-1)          # bad: a NaN row is visible
+            assert np.all(go[r][none] == 0) and np.all(np.isnan(go[r][bad]))
+            err, eo = np.linalg.norm(np.where(bad[..., None], 0, go[r] - o), axis=-1), np.where(bad, 0, eo)
+            none |= bad
+            assert np.all(err <= eo + 1e-30), (max_q, b, np.max(err / (eo + 1e-30)))
+            worst = max(worst, float(np.max(err / (eo + 1e-30))))
+            if lse_wanted:
+                assert np.all(np.isneginf(gl[r][none & ~bad]))
+                assert np.all(np.abs(gl[r][~none] - l[~none]) <= el[~none])
+        assert np.all(go[total:] == 7.0) and (gl is None or np.all(gl[total:] == 7.0))
     return worst
 
 
@@ -371,6 +385,8 @@ def test_split_rows_many(shape):
     attend_and_check(c, [40, 20, 3], 2)
     attend_and_check(c, [33, 1, 2], 2, window=900, prefix=[3, 0, 70], merge=True, cap=10.0)
     attend_and_check(c, [1, 1, 1], 1, max_len=10 ** 6)
+    attend_and_check(c, [70, 20, 3], 2, max_len=10 ** 6)         # many columns in ranges
+    attend_and_check(c, [65, 1, 2], 2, window=900, prefix=[3, 0, 70], merge=True, cap=10.0, max_len=10 ** 5)
 
 
 @pytest.mark.parametrize("shape", SHAPES, ids=IDS)
@@ -511,6 +527,7 @@ def test_tree(shape):
     attend_and_check(c, n, 2, tree=tree)
     attend_and_check(c, n, 1, tree=tree, cap=10.0, slopes=True, window=9, prefix=[2, 0, 0, 30])
     attend_and_check(c, n, 1, tree=tree, merge=True)
+    attend_and_check(c, n, 3, tree=tree, slopes=True, window=50, merge=True)
 
 
 def test_tree_masks_of_nothing():
@@ -723,6 +740,8 @@ def test_captured_prompt_tree_keep_and_read():
     def step(o, l, o2, a, b):
         c.gpu.append(k, v, st, n)
         c.gpu.attention(q, st, n, 1400, o, l, window=700)
+        c.gpu.attention(q, st, 1 << 16, 1400, o, l, window=700)
+        c.gpu.attention(q, st, 100, 1 << 17, o, l, window=700)
         c.gpu.tree_attention(q, st, n, 1400, masks, o2)
         c.gpu.keep(base, kst, path)
         c.gpu.read(first, rst, 70, a, b)
@@ -793,10 +812,11 @@ def test_queries_that_are_not_numbers(n):
         t, hq = c.torch, shape[0] * 2
         st, q = c.i32([0, n, 2 * n]), c.dev(np.random.default_rng(n).standard_normal((2 * n, hq, shape[1])), "bf16")
         clean, out = t.zeros_like(q), t.zeros_like(q)
-        c.gpu.attention(q, st, n, 150, clean)
+        bound = 1 if n == 1 else 1 << 16
+        c.gpu.attention(q, st, bound, 150, clean)
         q[0, 1, 5] = float("nan")
         q[n, 0, 60] = float("inf")
-        c.gpu.attention(q, st, n, 150, out)
+        c.gpu.attention(q, st, bound, 150, out)
         assert bool(out[0, 1].isnan().all()) and bool(out[n, 0].isnan().all())
         same = t.ones(2 * n, hq, dtype=t.bool, device="cuda")
         same[0, 1] = same[n, 0] = False
@@ -804,8 +824,8 @@ def test_queries_that_are_not_numbers(n):
         assert float((out - clean)[same].float().norm(dim=-1).max()) <= 2.0 ** -6 * float(clean.float().norm(dim=-1).max())
 
 
-@pytest.mark.parametrize("G", [1, 40])
-def test_nan_rows_that_stand_alone(G):
+@pytest.mark.parametrize("G,bound", [(1, 1), (40, 1), (40, 1000), (40, 40000)])
+def test_nan_rows_that_stand_alone(G, bound):
     """A visible NaN row is not lost where it is all that a row, a wave or a token range sees, nor where every
     other score is far above its part's."""
     for shape in (SHAPES[0], SHAPES[5]):
@@ -820,7 +840,7 @@ def test_nan_rows_that_stand_alone(G):
             c.append(bf16(k), v, [T])
             t = c.torch
             out = t.zeros(1, s.H * G, s.d, dtype=t.bfloat16, device="cuda")
-            c.gpu.attention(c.dev(q, "bf16"), c.i32([0, 1]), 1, T, out)
+            c.gpu.attention(c.dev(q, "bf16"), c.i32([0, 1]), bound, T, out)
             nan = out.isnan()
             assert bool(nan[:, :G].all()) and not bool(nan[:, G:].any())
 
@@ -848,7 +868,7 @@ def test_pages_past_4_gib(shape):
         g.keep(t.tensor([T - 20], dtype=t.int32, device="cuda"), t.tensor([0, 2], dtype=t.int32, device="cuda"),
                t.tensor([4, 3], dtype=t.int32, device="cuda"))
         outs = [t.zeros_like(q), t.zeros_like(q[:1]), t.zeros_like(k), t.zeros_like(v)]
-        g.attention(q, rows, n, T, outs[0])
+        g.attention(q, rows, 1 << 16, T, outs[0])
         g.attention(q[:1], t.tensor([0, 1], dtype=t.int32, device="cuda"), 1, T, outs[1])
         g.read(None, starts, T, outs[2], outs[3])
         t.cuda.synchronize()
