@@ -147,20 +147,55 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
     // following product, or two pieces of 8 in memory
     const int mtok = (m & 19) | ((m & 4) << 1) | ((m & 8) >> 1);
 
-    // ---- queries: lane (column m, half hh) has features 16 k + 8 hh + e of its row
+    // ---- the query rows' loads, on the way while the columns and the first tile are
+    // found: lane (column m, half hh) has features 16 k + 8 hh + e of its row
+    uint4 qraw[NK];
+    {
+        const int c = c0 + m, cq = c < ncol ? c : c0 < ncol ? ncol - 1 : 0;      // (a column past the last repeats one)
+        const uint16_t *row = static_cast<const uint16_t *>(a.q.ptr) + (int64_t)(s0 + cq / a.G) * a.q.ts +
+                              (h * a.G + cq % a.G) * a.q.hs + 8 * hh;
+#pragma unroll
+        for (int k = 0; k < NK; ++k) qraw[k] = *reinterpret_cast<const uint4 *>(row + 16 * k);
+    }
+
+    // ---- what the wave's columns see, and the workgroup's range of tiles
+    const int c = c0 + m;
+    const bool cv = c < ncol;
+    const Column mine(a, s0, n, base, len, prefix, h, c, cv);
+    if (hh == 0) reinterpret_cast<Column *>(cols)[32 * wave + m] = mine;
+    auto column = [&]() -> const Column & { return reinterpret_cast<const Column *>(cols)[32 * wave + m]; };
+    Reach reach(mine, cv);
+    reach.join<32>();
+    reach.clip(a, len, prefix);
+    reach.uniform();
+    if (lane == 0) {
+        reach_all[wave][0] = active ? reach.begin(prefix) : 0x7FFFFFFF;
+        reach_all[wave][1] = active ? reach.hi_any : 0;
+        reach_all[wave][2] = active ? reach.lo_any : 0x7FFFFFFF;
+    }
+    __syncthreads();
+    int begin = 0x7FFFFFFF, end = 0, lo_any = 0x7FFFFFFF;
+#pragma unroll
+    for (int x = 0; x < NW; ++x) {
+        begin = min(begin, reach_all[x][0]);
+        end = max(end, reach_all[x][1]);
+        lo_any = min(lo_any, reach_all[x][2]);
+    }
+    begin = __builtin_amdgcn_readfirstlane(begin);
+    end = __builtin_amdgcn_readfirstlane(end);
+    lo_any = __builtin_amdgcn_readfirstlane(lo_any);
+    const int tile0 = begin / kTile, ntile = end > begin ? (end + kTile - 1) / kTile - tile0 : 0;
+    const int per = max((ntile + a.splits - 1) / a.splits, a.least / kTile);
+    const int ts = tile0 + split * per, te = min(ts + per, tile0 + ntile);
+
+    const int P = 1 << a.c.page_shift;
+    const PageLayout pl = page_layout(P, D, BITS);
+    // ---- queries, divided by a power of two, in fp16
     f16x8 qf[NK];
     float qmul = 0.f;                                  // what the column's scores are multiplied with
-    {
-        const int c = c0 + m;
+    auto queries = [&]() {
         float x[NF][16];                               // features 32 i + 16 t + 8 hh + e at [i][8 t + e]
-        uint4 q[NK];
-        {
-            const int cq = c < ncol ? c : c0 < ncol ? ncol - 1 : 0;      // (a column past the last repeats one)
-            const uint16_t *row = static_cast<const uint16_t *>(a.q.ptr) + (int64_t)(s0 + cq / a.G) * a.q.ts +
-                                  (h * a.G + cq % a.G) * a.q.hs + 8 * hh;
-#pragma unroll
-            for (int k = 0; k < NK; ++k) q[k] = *reinterpret_cast<const uint4 *>(row + 16 * k);
-        }
+        uint4 (&q)[NK] = qraw;
         if constexpr (ROT) {
             // H (s o q) as a product with the +-1 matrix: exact bf16 operands, fp32 sums
 #pragma unroll
@@ -215,46 +250,13 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
             qf[k] = __builtin_bit_cast(f16x8, make_uint4(hi[0], hi[1], hi[2], hi[3]));
             if constexpr (kLo) *reinterpret_cast<uint4 *>(qlo + k * 1024) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
-    }
-
-    // ---- what the wave's columns see, and the workgroup's range of tiles
-    const int c = c0 + m;
-    const bool cv = c < ncol;
-    const Column mine(a, s0, n, base, len, prefix, h, c, cv);
-    if (hh == 0) reinterpret_cast<Column *>(cols)[32 * wave + m] = mine;
-    auto column = [&]() -> const Column & { return reinterpret_cast<const Column *>(cols)[32 * wave + m]; };
-    Reach reach(mine, cv);
-    reach.join<32>();
-    reach.clip(a, len, prefix);
-    reach.uniform();
-    if (lane == 0) {
-        reach_all[wave][0] = active ? reach.begin(prefix) : 0x7FFFFFFF;
-        reach_all[wave][1] = active ? reach.hi_any : 0;
-        reach_all[wave][2] = active ? reach.lo_any : 0x7FFFFFFF;
-    }
-    __syncthreads();
-    int begin = 0x7FFFFFFF, end = 0, lo_any = 0x7FFFFFFF;
-#pragma unroll
-    for (int x = 0; x < NW; ++x) {
-        begin = min(begin, reach_all[x][0]);
-        end = max(end, reach_all[x][1]);
-        lo_any = min(lo_any, reach_all[x][2]);
-    }
-    begin = __builtin_amdgcn_readfirstlane(begin);
-    end = __builtin_amdgcn_readfirstlane(end);
-    lo_any = __builtin_amdgcn_readfirstlane(lo_any);
-    const int tile0 = begin / kTile, ntile = end > begin ? (end + kTile - 1) / kTile - tile0 : 0;
-    const int per = max((ntile + a.splits - 1) / a.splits, a.least / kTile);
-    const int ts = tile0 + split * per, te = min(ts + per, tile0 + ntile);
-
-    const int P = 1 << a.c.page_shift;
-    const PageLayout pl = page_layout(P, D, BITS);
+    };
     f32x16 acc[NF];
 #pragma unroll
     for (int i = 0; i < NF; ++i) acc[i] = f32x16{};
     float mrun = neg_inf(), lrun = 0.f;
     int erun = kTop;                                   // exponent field of acc's unit, by column
-    const float mul = fminf(a.scale * kLog2e * qmul, 3e38f);     // (finite: a score of 0 stays 0)
+    float mul = 0.f;                                   // by column: log2 e times the scale
     const bool capped = a.cap > 0.f, sloped = a.slopes != nullptr, tree = a.tree != nullptr;
 
     // tiles between a prefix and the window are skipped by the whole workgroup
@@ -279,7 +281,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
     const bool second = __builtin_amdgcn_readfirstlane(wave) >= NW / 2;
     const uint32_t koff = (ktok & 31) * (D * BITS / 8) + ku0 * (4 * KU), voff = (vblk & 3) * (D * BITS) + vf * (4 * KU);
     const uint32_t all_off = (uint32_t)(hh ? pl.v_scales : pl.k_scales) + ((NG == 2 ? m >> 4 : 0) * P + 2 * (m & 15)) * 2;
-    Regs rg;
+    Regs rg, rg2;                                      // (rg2: the first tile)
     // The loads go through buffer descriptors of the two page blocks: a uniform
     // base, a uniform offset and one 32-bit offset a lane, bounded by the block.
     auto block = [&](int page) {
@@ -287,40 +289,56 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
         const uint8_t *p = a.c.pool + (page >= 0 ? cache_block_offset(a.c, page, h) : 0);
         return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), 0, (int)pl.bytes, 0x00027000);
     };
-    auto fetch = [&](int t, int p0, int p1) {
+    auto r0 = block(-1), r1 = r0;                      // the tile's halves
+    constexpr int kFetch = 4;                          // parts of a fetch
+    auto fetch_part = [&](Regs &rg, int part, int t, int p0, int p1) {
         const int t0 = t * kTile, i0 = t0 & (P - 1), i1 = (t0 + 32) & (P - 1), iw = second ? i1 : i0;
-        const auto bw = block(second ? p1 : p0);
-        constexpr int N = UPT * KU;
-        if constexpr (N == 1) rg.k[0] = __builtin_amdgcn_raw_buffer_load_b32(bw, koff, iw * (D * BITS / 8), 0);
-        else if constexpr (N == 2) {
-            const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(bw, koff, iw * (D * BITS / 8), 0);
-            rg.k[0] = v.x; rg.k[1] = v.y;
-        } else {
+        if (part == 0) {
+            r0 = block(p0);
+            r1 = block(p1);
+        }
+        const auto bw = second ? r1 : r0;
+        if (part == 1) {
+            constexpr int N = UPT * KU;
+            if constexpr (N == 1) rg.k[0] = __builtin_amdgcn_raw_buffer_load_b32(bw, koff, iw * (D * BITS / 8), 0);
+            else if constexpr (N == 2) {
+                const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(bw, koff, iw * (D * BITS / 8), 0);
+                rg.k[0] = v.x; rg.k[1] = v.y;
+            } else {
 #pragma unroll
-            for (int i = 0; i < N; i += 4) {
-                const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(bw, koff + 4 * i, iw * (D * BITS / 8), 0);
-                rg.k[i] = v.x; rg.k[i + 1] = v.y; rg.k[i + 2] = v.z; rg.k[i + 3] = v.w;
+                for (int i = 0; i < N; i += 4) {
+                    const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(bw, koff + 4 * i, iw * (D * BITS / 8), 0);
+                    rg.k[i] = v.x; rg.k[i + 1] = v.y; rg.k[i + 2] = v.z; rg.k[i + 3] = v.w;
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < NG; ++q)
+                rg.ks[q] = __builtin_amdgcn_raw_buffer_load_b16(bw, (ktok & 31) * 2, (int)pl.k_scales + (q * P + iw) * 2, 0);
+        }
+        if (part == 2) {
+#pragma unroll
+            for (int x = 0; x < UPT; ++x) {
+                const int so = (int)pl.v_codes + (iw >> 3) * (D * BITS);
+                if constexpr (KU == 1) rg.v[x] = __builtin_amdgcn_raw_buffer_load_b32(bw, voff + FS * x * 4, so, 0);
+                else {
+                    const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(bw, voff + FS * x * 8, so, 0);
+                    rg.v[2 * x] = v.x; rg.v[2 * x + 1] = v.y;
+                }
             }
         }
+        if (part == 3) {
 #pragma unroll
-        for (int q = 0; q < NG; ++q)
-            rg.ks[q] = __builtin_amdgcn_raw_buffer_load_b16(bw, (ktok & 31) * 2, (int)pl.k_scales + (q * P + iw) * 2, 0);
-#pragma unroll
-        for (int x = 0; x < UPT; ++x) {
-            const int so = (int)pl.v_codes + (iw >> 3) * (D * BITS);
-            if constexpr (KU == 1) rg.v[x] = __builtin_amdgcn_raw_buffer_load_b32(bw, voff + FS * x * 4, so, 0);
-            else {
-                const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(bw, voff + FS * x * 8, so, 0);
-                rg.v[2 * x] = v.x; rg.v[2 * x + 1] = v.y;
+            for (int q = 0; q < NG; ++q) {
+                const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(bw, (vblk & 3) * 16, (int)pl.v_scales + (q * P + iw) * 2, 0);
+                rg.vs[q][0] = v.x; rg.vs[q][1] = v.y; rg.vs[q][2] = v.z; rg.vs[q][3] = v.w;
             }
+            rg.all[0] = __builtin_amdgcn_raw_buffer_load_b32(r0, all_off, i0 * 2, 0);
+            rg.all[1] = __builtin_amdgcn_raw_buffer_load_b32(r1, all_off, i1 * 2, 0);
         }
+    };
+    auto fetch = [&](Regs &rg, int t, int p0, int p1) {
 #pragma unroll
-        for (int q = 0; q < NG; ++q) {
-            const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(bw, (vblk & 3) * 16, (int)pl.v_scales + (q * P + iw) * 2, 0);
-            rg.vs[q][0] = v.x; rg.vs[q][1] = v.y; rg.vs[q][2] = v.z; rg.vs[q][3] = v.w;
-        }
-        rg.all[0] = __builtin_amdgcn_raw_buffer_load_b32(block(p0), all_off, i0 * 2, 0);
-        rg.all[1] = __builtin_amdgcn_raw_buffer_load_b32(block(p1), all_off, i1 * 2, 0);
+        for (int x = 0; x < kFetch; ++x) fetch_part(rg, x, t, p0, p1);
     };
     // Of the scales of K (lane 31) and of V (lane 63): the largest in the lower half,
     // the smallest that is not 0 in the upper one, negated, so that one maximum over
@@ -342,7 +360,8 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
     uint32_t magic = 0x64006400u;
     asm("" : "+v"(magic));
     struct Tile { int t, p0, p1, ek, ev, wild; };
-    auto stage = [&](Tile &tile, uint8_t *kbuf, uint8_t *vbuf) {
+    uint32_t kbad = 0, kdown = 0, vdown[4];
+    auto units = [&](Regs &rg, Tile &tile, uint8_t *vbuf) {
         const int t0 = tile.t * kTile;
         const int lim0 = tile.p0 >= 0 ? len : 0, lim1 = tile.p1 >= 0 ? len : 0;      // tokens below these count, by half
         const bool whole = t0 + kTile <= min(lim0, lim1);
@@ -355,7 +374,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
         uint32_t x = extremes(all0, all1);
         uint32_t xk = lane_of(x, 31), xv = lane_of(x, 63);
         const bool clean = whole && max(xk & 0xFFFFu, xv & 0xFFFFu) < 0x7F80u;
-        uint32_t kbad = 0;
+        kbad = 0;
         const int limw = second ? lim1 : lim0, tk = t0 + ktok, tv = t0 + 8 * vblk;
         if (!clean) {
             // a tile with a last token, a missing half or a NaN scale inside: scales
@@ -397,8 +416,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
         tile.wild = jump || (!kPost && lk < ek - 18) || lv < vu - 18;
         tile.ek = ek;
         tile.ev = tile.wild ? ev : vu;
-        uint32_t kdown = (uint32_t)(ek - kTop) * 0x00800080u;
-        uint32_t vdown[4];
+        kdown = (uint32_t)(ek - kTop) * 0x00800080u;
 #pragma unroll
         for (int i = 0; i < 4; ++i) vdown[i] = (uint32_t)(vu - kTop) * 0x00800080u;
         if (tile.wild) {
@@ -419,9 +437,11 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
                 }
             }
         }
-#pragma unroll
-        for (int x = 0; x < UPT; ++x) {
-            const int u = ku0 + x, g = u / (D / 32), kk = u % (D / 32);
+    };
+    // registers -> LDS, in 2 UPT parts: the thread's units of K, then those of V
+    auto put = [&](const Regs &rg, int part, uint8_t *kbuf, uint8_t *vbuf) {
+        if (part < UPT) {
+            const int x = part, u = ku0 + x, g = u / (D / 32), kk = u % (D / 32);
             f16x2 y[4];
             unit_f16<BITS>(&rg.k[x * KU], magic, y);
             if constexpr (!kPost) {
@@ -433,26 +453,19 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
             }
             *reinterpret_cast<uint4 *>(kbuf + (4 * kk + g) * kKStride + ktok * 16) =
                 make_uint4(u32(y[0]), u32(y[1]), u32(y[2]), u32(y[3]));
-        }
-        if constexpr (kPost) {
-            if (ku0 == 0)
+            if constexpr (kPost) {
+                if (part == 0 && ku0 == 0)
 #pragma unroll
-                for (int q = 0; q < NG; ++q)
-                    reinterpret_cast<float *>(vbuf + kVBytes)[q * kTile + ktok] =
-                        kbad ? __builtin_nanf("") : bf16_to_f32(rg.ks[q]);
-        }
-        f16x2 sc[NG][4];
-#pragma unroll
-        for (int q = 0; q < NG; ++q)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sc[q][i] = scale_f16(rg.vs[q][i], vdown[i]);
-#pragma unroll
-        for (int x = 0; x < UPT; ++x) {
+                    for (int q = 0; q < NG; ++q)
+                        reinterpret_cast<float *>(vbuf + kVBytes)[q * kTile + ktok] =
+                            kbad ? __builtin_nanf("") : bf16_to_f32(rg.ks[q]);
+            }
+        } else {
+            const int x = part - UPT, q = NG == 1 ? 0 : (FS * x) / 64;
             f16x2 y[4];
             unit_f16<BITS>(&rg.v[x * KU], magic, y);
-            const int q = NG == 1 ? 0 : (FS * x) / 64;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) y[i] *= sc[q][i];
+            for (int i = 0; i < 4; ++i) y[i] *= scale_f16(rg.vs[q][i], vdown[i]);
             *reinterpret_cast<uint4 *>(vbuf + (vblk * D + vf + FS * x) * 16) =
                 make_uint4(u32(y[0]), u32(y[1]), u32(y[2]), u32(y[3]));
         }
@@ -462,13 +475,15 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
 
     // Two groups of waves, one on each half of every SIMD's slots, take turns at
     // the matrix cores: while one multiplies (weights of its last tile times V,
-    // then queries times the K of the next), the other runs softmax and staging
-    // on the vector unit; a barrier ends each turn.
-    //   turn    2 i - 2        2 i - 1        2 i            2 i + 1
-    //   early   M(i-1)         V(i-1) st(i)   M(i)           V(i) st(i+1)
-    //   late    V(i-2) st(i)   M(i-1)         V(i-1) st(i+1) M(i)
-    // Both halves of tile i are staged before turn 2 i.  A turn that stages tile
-    // i overlaps products on K(i-1) and V(i-2): two K buffers, three V buffers.
+    // then queries times the K of the next) and writes its half of the tile after
+    // to LDS in between, the other runs softmax on the vector unit and finds the
+    // units of the tile after that; a barrier ends each turn.
+    //   turn    2 i           2 i + 1        2 i + 2        2 i + 3
+    //   early   M(i) put i+1  V(i) units i+2 M(i+1) put i+2 V(i+1)
+    //   late    V(i-1)        M(i) put i+1   V(i) units i+2 M(i+1) put i+2
+    // M(i) multiplies with V(i-1) and K(i).  Tile i + 1 is whole before turn 2 i + 2,
+    // and is put in turns 2 i and 2 i + 1 where K(i), V(i-1) are read and, by then
+    // done with, K(i-1) and V(i-2) were: two K buffers, three V buffers.
     const bool late = second;
     auto look = [&](int t) {
         if (t >= te) return Tile{t, -1, -1, kTop, kTop, 0};
@@ -478,18 +493,15 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
         }
         return Tile{t, page_of(t, 0), page_of(t, 1), kTop, kTop, 0};
     };
-    // field by field: a choice between the structs themselves would put them in memory
-    auto of_group = [&](Tile e, Tile l) {
-        return Tile{late ? l.t : e.t, late ? l.p0 : e.p0, late ? l.p1 : e.p1, late ? l.ek : e.ek, late ? l.ev : e.ev,
-                    late ? l.wild : e.wild};
-    };
-    auto stage_tile = [&](Tile &x, int nth) { stage(x, lds + (nth & 1) * kKBytes, vlds + (nth % 3) * kVBuf); };
+    auto kbuf_of = [&](int nth) { return lds + (nth & 1) * kKBytes; };
+    auto vbuf_of = [&](int nth) { return vlds + (nth % 3) * kVBuf; };
     f32x16 s[2];
     f16x8 pf[4];
     // In both products the next step's fragments are read from LDS before the
     // present step's products are issued, in the order written here.
     auto times_v = [&](int nth) {
-        const uint8_t *vb = vlds + (nth % 3) * kVBuf;
+        const uint8_t *vb = vbuf_of(nth);
+        uint8_t *const kput = kbuf_of(nth + 2), *const vput = vbuf_of(nth + 2);
         constexpr int A = 5;                           // pairs of fragments held: four ahead of the one in use
         f16x8 f[A][2];
         auto read = [&](int g) {                       // pair g: block of tokens g / (NF/2), features of 2 (g % (NF/2))
@@ -499,6 +511,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
                     vb + ((2 * (g / (NF / 2)) + hh) * D + 32 * (2 * (g % (NF / 2)) + i) + m) * 16);
         };
         constexpr int N = 4 * NF / 2;
+        static_assert(N == 4 * UPT);
 #pragma unroll
         for (int g = 0; g < A - 1; ++g) read(g);
 #pragma unroll
@@ -510,10 +523,12 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
                 const int x = 2 * (g % (NF / 2)) + i;
                 acc[x] = mfma32(f[g % A][i], pf[g / (NF / 2)], acc[x]);
             }
+            if (g & 1) put(rg, g >> 1, kput, vput);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    auto times_k = [&](int nth) {
+    // between: what else is issued after step k's products
+    auto times_k = [&](int nth, auto between) {
         const uint8_t *kb = lds + (nth & 1) * kKBytes;
         // x[u] += K rows of half u times the queries, features 16 k0 .. 16 k1 - 1
         auto products = [&](f32x16 (&x)[2], int k0, int k1) {
@@ -536,6 +551,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
                 if constexpr (kLo)
 #pragma unroll
                     for (int u = 0; u < 2; ++u) x[u] = mfma32(kf[k % A][u], ql[k % A], x[u]);
+                between(k);
                 __builtin_amdgcn_sched_barrier(0);
             }
         };
@@ -567,26 +583,27 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
         seen = first_tile;
         load_pages();
         Tile cur = look(first_tile), nxt = look(next_tile(first_tile + 1));
-        fetch(cur.t, cur.p0, cur.p1);
-        stage_tile(cur, 0);
-        if (late) {
-            fetch(nxt.t, nxt.p0, nxt.p1);
-            stage_tile(nxt, 1);
-        }
+        fetch(rg2, cur.t, cur.p0, cur.p1);
+        fetch(rg, nxt.t, nxt.p0, nxt.p1);
+        queries();
+        mul = fminf(a.scale * kLog2e * qmul, 3e38f);   // (finite: a score of 0 stays 0)
+        units(rg2, cur, vbuf_of(0));
+#pragma unroll
+        for (int x = 0; x < 2 * UPT; ++x) put(rg2, x, kbuf_of(0), vbuf_of(0));
+        units(rg, nxt, vbuf_of(1));
         Tile nx2 = look(next_tile(nxt.t + 1));
         __syncthreads();
         if (late) __syncthreads();                     // the late group's first turn: early multiplies
-        {
-            const Tile f = of_group(nxt, nx2);
-            fetch(f.t, f.p0, f.p1);
-        }
-        times_k(0);
+#pragma unroll
+        for (int x = 0; x < 2 * UPT; ++x) put(rg, x, kbuf_of(1), vbuf_of(1));
+        fetch(rg, nx2.t, nx2.p0, nx2.p1);
+        times_k(0, [](int) {});
         erun = cur.ev;
         __syncthreads();
         for (int i = 0;; ++i) {
             const int t0 = cur.t * kTile;
             const Tile nx3 = look(next_tile(nx2.t + 1));
-            // ---- V: softmax of this tile, staging of a later one
+            // ---- V: softmax of this tile, units of a later one
             const float *km = reinterpret_cast<const float *>(vlds + (i % 3) * kVBuf + kVBytes + kSBytes) + 8 * hh;
             float kunit = kPost ? 1.f : __builtin_ldexpf(1.f, cur.ek - 127 - (kTop - 15));   // 2^E
             if (!kPost && cur.wild) {                  // a unit for every token
@@ -725,24 +742,17 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
                                                              f16_pair(p[o + 4], p[o + 5]), f16_pair(p[o + 6], p[o + 7])));
                 asm volatile("" : "+v"(pf[x]), "+v"(lrun));   // computed in this turn, not sunk into the next
             }
-            Tile st = of_group(nxt, nx2);
-            stage_tile(st, late ? i + 2 : i + 1);
-            nxt.ek = late ? nxt.ek : st.ek;
-            nxt.ev = late ? nxt.ev : st.ev;
-            nxt.wild = late ? nxt.wild : st.wild;
-            nx2.ek = late ? st.ek : nx2.ek;
-            nx2.ev = late ? st.ev : nx2.ev;
-            nx2.wild = late ? st.wild : nx2.wild;
+            units(rg, nx2, vbuf_of(i + 2));
             __syncthreads();
-            // ---- M: products
+            // ---- M: products, and tile i + 2 to LDS
             const bool last = nxt.t >= te;
-            if (!last) {
-                const Tile f = of_group(nx2, nx3);
-                fetch(f.t, f.p0, f.p1);
-            }
+            __builtin_amdgcn_s_setprio(1);             // before the other group's vector work
             times_v(i);
             if (last) break;
-            times_k(i + 1);
+            times_k(i + 1, [&](int k) {
+                if (k % (NK / kFetch) == 0) fetch_part(rg, k / (NK / kFetch), nx3.t, nx3.p0, nx3.p1);
+            });
+            __builtin_amdgcn_s_setprio(0);
             __syncthreads();
             cur = nxt;
             nxt = nx2;
