@@ -17,6 +17,18 @@
 // product takes its P^T operand in, so weights never leave registers.  Softmax
 // runs in one pass with a running maximum per column, which is raised, and the
 // sums rescaled, only when a score passes it by 2^8.
+//
+// Roundings: K and V codes are exact; a rotated query is held in two bf16 parts
+// (one part alone would err by 2^-9 of every feature, and the scores with it); a
+// weight times its value scale is rounded to bf16, because the product takes it so:
+// 2^-9 of each summand, as in any attention on 16-bit weights.
+//
+// Bound by the reads of the cache for one token a sequence, and at long ranges by
+// how many are in flight: two blocks of 32 tokens a wave, two workgroups a CU.
+// d = 128, 8 heads, 32 query heads: 16 x 8192 tokens of 8 bits 51 us with the join
+// (3.2 TB/s; a large copy 5.1), 65535 tokens of 4 bits 26.6 us (2.7 TB/s).  At 32
+// and more columns the vector work that turns codes into bf16 is done again for
+// every 16 columns and bounds it: 61 us for 48 columns over 16 x 4096 tokens.
 #include <algorithm>
 
 #include "cache.h"
@@ -86,7 +98,8 @@ __device__ __forceinline__ constexpr int value_feature(int i, int m) {
 // sequence); column c of a sequence's KV head is query row c / G, head h G +
 // c % G.  The waves take the range's 32-token blocks in turn (each block's
 // fragments go from memory to registers, the next block's while this one is
-// computed) and join their sums through LDS at the end.
+// computed) and join their sums through LDS at the end.  No tile goes through LDS:
+// with 16 columns each fragment is used by one wave once.
 template <int D, int BITS, bool ROT>
 __global__ __launch_bounds__(64 * kWaves, 2) void k_cache_attn(CacheAttnArgs a, int ctiles) {
     constexpr int NK = D / 32, NV = D / 16, NG = D / 64, KU = BITS / 4;
@@ -378,7 +391,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_cache_attn(CacheAttnArgs a, 
 // which the row saw nothing (m_s = -inf) has no sums in the workspace.  Rows are
 // addressed through the sequences, so rows that no sequence has stay as they are.
 
-// Up to kFew ranges: D / 8 lanes take a row's ranges one after the other.
+// Up to kFew ranges: D / 8 lanes take a row's ranges one after the other.  Bound by
+// the launch and a chain of loads: 3.4 us for a decode step of 16 sequences, 5.8
+// for the 48 rows each of 16 trees.
 constexpr int kFew = 16;
 template <int D, bool ROT>
 __global__ __launch_bounds__(256) void k_cache_attn_join(CacheAttnArgs a, int nblk) {
@@ -413,7 +428,8 @@ __global__ __launch_bounds__(256) void k_cache_attn_join(CacheAttnArgs a, int nb
 
 // More: one workgroup of 256 threads per row.  Every thread first takes one
 // range's m and l, so that all weights are known after one read; then 2048 / D
-// groups of D / 8 lanes sum the ranges in turn and are added through LDS.
+// groups of D / 8 lanes sum the ranges in turn and are added through LDS.  64
+// ranges of a 64 k cache: 4.1 us.
 constexpr int kMaxSplits = 256;
 template <int D, bool ROT>
 __global__ __launch_bounds__(256) void k_cache_attn_join_many(CacheAttnArgs a) {

@@ -1,19 +1,40 @@
 // Attention over the token cache for many query rows (prompt chunks, trees):
-// the same sums as k_cache_attn.hip, with 64-token tiles of the cache staged
-// once per workgroup in LDS and shared by its waves of 32 query columns.
+// the same sums as k_cache_attn.hip, with 64-token tiles of the cache put into LDS
+// once per workgroup and shared by its 8 waves of 32 query columns.
 //
-// Staging undoes the quantization, so that a score costs one product and no
-// scaling: rows go to LDS in fp16 as q sc 2^-E, with E the tile's largest scale
-// exponent.  For 4-bit codes that is exact (3 + 8 significant bits); for 8-bit
-// ones K holds the codes alone (their scales multiply the scores of each group
-// of 64 in fp32) and V is rounded to fp16 (2^-11).  A scale more than 2^26
-// (4 bits; 8 bits: 2^22) below the tile's largest counts as nothing.  Queries
-// are divided by a power of two that brings their largest feature to [1, 2) and
-// held in fp16: exact for bf16 queries, two parts (2^-22) for rotated ones.
-// Weights are rounded to fp16 (2^-11).
+// On the way to LDS the quantization is undone, so that a score costs one product
+// and no scaling: rows are held in fp16 as q sc 2^-E, with E a scale exponent of
+// the tile.  For 4-bit codes that is exact (3 + 8 significant bits) down to 2^-18
+// of the tile's largest scale; for 8-bit ones K holds the codes alone (their scales
+// multiply the scores of each group of 64 in fp32) and V is rounded to fp16
+// (2^-11).  E of K is its largest scale's; E of V is kept from tile to tile while
+// it fits, because the sums are in its unit.  A tile whose scales lie further
+// apart, or jump, is "wild": every token has a unit of its own there, kept beside
+// the tile, which multiplies its scores and weights, and each column's sum changes
+// to the unit that its largest weight asks for.
+// Queries are divided by a power of two that brings their largest feature to [1, 2)
+// and held in fp16: exact for bf16 queries (below 2^-16 of the largest, to 2^-25 of
+// it), two parts (2^-22) for rotated ones (one part alone takes a fifth off the
+// time, and puts 5e-6 on the log-sum-exp where two leave 3e-7).  Weights are rounded
+// to fp16 (2^-11); what falls below 2^-24 of the column's largest is lost.
 //
 // Products are S^T = K Q^T and O^T = V^T P^T in 32x32x16, and as in the narrow
 // kernel a lane's scores are, in order, its operand of the second product.
+//
+// LDS (158 KB at d = 128, rotated): two K buffers, three V buffers, the queries'
+// second parts, the columns' limits; the first parts, the sums, scores and weights
+// are in registers (227-256 a lane), so a CU holds one workgroup, two waves a SIMD.
+//
+// Bound by the matrix unit and the vector unit in turn: 2048 rows x 32 heads at the
+// end of 8192 tokens, d = 128, 4 bits, rotated: 348 us, 689 TFLOP/s of plain
+// attention and 1.5 times that in products (matrix pipes busy 56 % of the cycles;
+// a large bf16 product reaches 1240 TFLOP/s).  A turn of products takes about 2700
+// cycles where its 48 instructions need 1536, a turn of softmax and units 2400.
+// Measured steps: 8 waves without turns 412 us; turns 375; tiles and loads between
+// the products and s_setprio 348.  48 drafted rows x 32 heads of 16 sequences over
+// 4144 tokens 96 us (192 of 256 columns are there); 4 x 509 packed rows of 40 heads,
+// window 1024, 8 bits 72 us (320 workgroups on 256 CUs, of which 17 us is each one's
+// start and end).
 #include <algorithm>
 
 #include "cache.h"
@@ -746,7 +767,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_cache_attn_wide(CacheAttnArgs a,
             __syncthreads();
             // ---- M: products, and tile i + 2 to LDS
             const bool last = nxt.t >= te;
-            __builtin_amdgcn_s_setprio(1);             // before the other group's vector work
+            __builtin_amdgcn_s_setprio(1);             // before the other group's vector work: 434 -> 415 us
             times_v(i);
             if (last) break;
             times_k(i + 1, [&](int k) {
