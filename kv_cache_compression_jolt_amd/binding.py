@@ -547,6 +547,13 @@ class JoltCache:
     def _stream(self):
         return self.torch._C._cuda_getCurrentRawStream(self.device.index)
 
+    def _capturing(self):
+        torch = self.torch
+        if torch.cuda.current_device() == self.device.index:
+            return torch.cuda.is_current_stream_capturing()
+        with torch.cuda.device(self.device):
+            return torch.cuda.is_current_stream_capturing()
+
     def append(self, k, v, starts, max_new):
         """Write rows k, v [total, H, d] (bf16 or fp32) as the last tokens of their sequences."""
         rk, rv, dt = self._kv(k, v)
@@ -594,8 +601,7 @@ class JoltCache:
         sp = self._tensor("starts", starts, i32, 1, self.batch + 1)
         stream = self._stream()
         own = workspace is None
-        with torch.cuda.device(self.device):
-            capturing = own and torch.cuda.is_current_stream_capturing()
+        capturing = own and self._capturing()
         if own and not capturing:
             have = self.workspaces.get(stream)
             workspace = have[-1] if have else None
