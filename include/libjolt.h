@@ -374,7 +374,8 @@ typedef struct {
  * starts[b+1] - 1 are the last tokens of sequence b (one for a decode step, or
  * a chunk of a prompt, appended before).  max_q: no sequence has more rows
  * (rows beyond it are left out).  max_len: the longest sequence as far as the
- * host knows; it sets how far the work is split, not what is read.
+ * host knows; with max_q it sets which kernel runs and how far the work is
+ * split, not what is read, so loose bounds cost time only.
  *   out  bf16 rows;  lse  device fp32 [total][q_heads], NULL = not wanted
  * Rows past starts[batch] of out and lse are left as they are.  K enters the
  * products exactly; rotated queries are held in two parts (2^-16 or better);
